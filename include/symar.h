@@ -37,7 +37,7 @@
  *    as SYM_ERR_TIMEOUT from sym_stream_status(); sym_last_error() then names
  *    the wait site: 1 signal wait, 2 counter wait, 3 pull-tile flag, 4 put +
  *    signal / AlltoAll receiver, 5 bulk-copy stage, 6 put + signal batch
- *    order, 7 barrier.  No call traps the GPU.
+ *    order, 7 barrier, 9 linear stage.  No call traps the GPU.
  *  - Windows are owned by the library (sym_window_alloc) or by the caller
  *    (sym_window_register).  Free a window only after every stream that used
  *    it has finished with it; windows must be freed before unloading.
@@ -73,6 +73,8 @@ typedef enum {
 
 typedef enum { SYM_F32 = 0, SYM_BF16 = 1, SYM_F16 = 2 } sym_dtype_t;
 typedef enum { SYM_SUM = 0, SYM_MAX = 1, SYM_MIN = 2 } sym_op_t;
+
+typedef enum { SYM_ACT_NONE = 0, SYM_ACT_RELU = 1, SYM_ACT_GELU = 2, SYM_ACT_SILU = 3 } sym_act_t;
 
 typedef enum {
     SYM_ALGO_AUTO = 0,
@@ -378,6 +380,129 @@ sym_status_t sym_counter_read(sym_win_t w, int rank, uint32_t counter_id, int bi
 sym_status_t sym_counter_wait(sym_win_t w, int rank, uint32_t counter_id, uint64_t least, int bits,
                               uint64_t timeout_ns, sym_stream_t stream);
 sym_status_t sym_counter_reset(sym_win_t w, int rank, uint32_t counter_id, sym_stream_t stream);
+
+/* ---------------------------------------------------------------- training step
+ *
+ * The operators that stand before and after the gradients' AllReduce in a
+ * data-parallel training step: the layer and the loss that make the gradients
+ * (a rank's window can be `dw` directly) and the optimizer step that uses
+ * their sum.  Pointers are device pointers of the current device; the calls
+ * enqueue on `stream`, allocate nothing (but sym_adamw_create) and keep
+ * nothing between calls.  Workspaces are the caller's: 256-byte aligned, not
+ * shared by calls in flight at once, free to reuse once the call's work has
+ * ended.  `ld*` are row strides in elements.  Inputs and outputs share no
+ * byte unless a call says so.
+ */
+
+/* Linear layer: z = x w^T + bias, y = act(z) + residual.  x is M x K, w is
+ * N x K, y, residual and pre are M x N, bias has N elements, all of `dtype`;
+ * bias, residual and pre may be NULL.  `pre`, if given, receives z (for the
+ * backward call).  Sums are held in 32 bits and rounded once to `dtype`.
+ * act: none, relu, gelu = z/2 (1 + erf(z/sqrt 2)), silu = z/(1 + exp(-z)).
+ * M = 0 or N = 0 does nothing; K = 0 leaves act(bias) + residual.  y may be
+ * `residual` itself (same pointer and stride).  BF16 and F16 run on the
+ * tensor cores, F32 on the FMA units.  `workspace` holds operands whose rows
+ * are not 16-byte aligned, copied to rows that are; sym_linear_workspace says
+ * how many bytes it has to have (0 when every row is aligned).
+ * Errors: INVALID_ARG, UNSUPPORTED (a size of 2^31 or more), CUDA. */
+size_t sym_linear_workspace(const void* x, size_t ldx, const void* w, size_t ldw, size_t M, size_t N,
+                            size_t K, sym_dtype_t dtype);
+sym_status_t sym_linear(const void* x, size_t ldx, const void* w, size_t ldw, const void* bias,
+                        const void* residual, size_t ldr, void* y, size_t ldy, void* pre, size_t ldp,
+                        size_t M, size_t N, size_t K, sym_dtype_t dtype, sym_act_t act,
+                        void* workspace, size_t workspace_bytes, sym_stream_t stream);
+
+/* Its gradients: dz = dy * act'(pre); dx = dz w (M x K, `dtype`);
+ * dw = dz^T x (N x K) and dbias = sum over rows of dz (N), both of
+ * `grad_dtype` (`dtype` or F32), added to what is there when `accumulate` is
+ * not 0.  The residual's gradient is dy itself.  Any of dx, dw, dbias may be
+ * NULL; `pre` (the z of the forward call) is needed unless act is NONE.  The
+ * two products take dz rounded to `dtype`, dbias sums it unrounded.  M = 0
+ * makes dw and dbias 0 (or leaves them, accumulating).  The sums' order does
+ * not depend on timing: equal calls give equal bits.
+ * Errors: as sym_linear. */
+size_t sym_linear_backward_workspace(size_t M, size_t N, size_t K, sym_dtype_t dtype, sym_act_t act);
+sym_status_t sym_linear_backward(const void* dy, size_t lddy, const void* x, size_t ldx, const void* w,
+                                 size_t ldw, const void* pre, size_t ldp, void* dx, size_t lddx,
+                                 void* dw, size_t lddw, void* dbias, size_t M, size_t N, size_t K,
+                                 sym_dtype_t dtype, sym_dtype_t grad_dtype, sym_act_t act,
+                                 int accumulate, void* workspace, size_t workspace_bytes,
+                                 sym_stream_t stream);
+
+/* Clipped policy loss with a KL term, from logits (rows x vocab, `dtype`).
+ * For a row with weight w != 0 and z = logits / temperature, y = target:
+ *   lse = log sum_j exp(z_j), logp = z_y - lse, rho = exp(logp - old_logp),
+ *   loss += w (-min(rho A, clip(rho, 1 - clip_low, 1 + clip_high) A)
+ *              + kl_coef (exp(k) - k - 1)),   k = ref_logp - logp,
+ * both exponents clamped to [-20, 20] (no gradient beyond).  ref_logp NULL
+ * leaves the KL term out; weights NULL means 1 each (a token mean passes
+ * 1/count).  A row of weight 0 is not read and gives zeros, whatever its
+ * logits are; so does a row whose target is no column, which also sets the
+ * device status (SYM_ERR_DEVICE_STATUS from sym_stream_status).
+ * stats[4] = loss, policy part, sum w kl, sum of w over clipped rows; logp
+ * and lse (rows each, F32) are kept for the backward call.  dlogits, if not
+ * NULL, receives *grad_out (NULL = 1) times the loss's gradient in the same
+ * pass; it may be `logits` itself (same pointer and stride).  rows = 0 gives
+ * stats of 0.  Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
+sym_status_t sym_policy_loss(const void* logits, size_t ld, size_t rows, size_t vocab, sym_dtype_t dtype,
+                             const int64_t* targets, const float* old_logp, const float* ref_logp,
+                             const float* advantages, const float* weights, double clip_low,
+                             double clip_high, double kl_coef, double temperature, float* stats,
+                             float* logp, float* lse, void* dlogits, size_t ldd, const float* grad_out,
+                             sym_stream_t stream);
+
+/* The gradient alone, from the logp and lse that sym_policy_loss left. */
+sym_status_t sym_policy_loss_backward(const void* logits, size_t ld, size_t rows, size_t vocab,
+                                      sym_dtype_t dtype, const int64_t* targets, const float* old_logp,
+                                      const float* ref_logp, const float* advantages,
+                                      const float* weights, double clip_low, double clip_high,
+                                      double kl_coef, double temperature, const float* logp,
+                                      const float* lse, void* dlogits, size_t ldd, const float* grad_out,
+                                      sym_stream_t stream);
+
+typedef struct sym_adamw* sym_adamw_t;   /* opaque: the tensors an AdamW step goes over */
+
+/* Collect `ntensors` tensors of counts[i] elements (0 allowed) for AdamW
+ * steps.  params[i] and grads[i] are of param_dtype and grad_dtype.  With
+ * exp_avg_scale and exp_avg_sq_scale NULL the states are F32 (exp_avg_sq
+ * holds v).  Otherwise they are 8-bit: exp_avg[i] and exp_avg_sq[i] hold
+ * e4m3 codes, of m and of sqrt(v), and the scale arrays one byte s per 32
+ * elements (the last block may be short), the block's values being
+ * code * 2^(s-127); all zero is a valid start.  copies (or NULL) get the new
+ * parameters rounded to copy_dtype.  The pointer arrays are read during the
+ * call, the tensors belong to the caller and have to outlive the handle.
+ * Elements are numbered through all tensors, each tensor starting at the
+ * next multiple of 32 (these numbers draw the stochastic rounding).
+ * Allocates the table of tensors on the current device, synchronising it.
+ * Errors: INVALID_ARG, UNSUPPORTED, OOM, CUDA. */
+sym_status_t sym_adamw_create(size_t ntensors, const size_t* counts, void* const* params,
+                              const void* const* grads, void* const* exp_avg, void* const* exp_avg_sq,
+                              void* const* exp_avg_scale, void* const* exp_avg_sq_scale,
+                              void* const* copies, sym_dtype_t param_dtype, sym_dtype_t grad_dtype,
+                              sym_dtype_t copy_dtype, sym_adamw_t* out);
+
+/* One AdamW step (step >= 1) over all tensors in one launch, in place:
+ *   g = grad * *grad_scale (device scalar; NULL = 1)
+ *   m = m b1 + g (1-b1), v = v b2 + g^2 (1-b2)
+ *   p = p (1 - lr wd) - lr/(1-b1^step) * m / (sqrt(v) / sqrt(1-b2^step) + eps)
+ * in F32, each operation rounded once.  A *grad_scale that is not finite
+ * skips the step as a whole (nothing is written).  8-bit states: m is rounded
+ * to nearest, sqrt(v) stochastically by 20 bits mixed from (seed, element
+ * number), so pass another seed each step (the step number will do); equal
+ * seeds give equal bits.  Calls on one handle go on one stream.
+ * Errors: INVALID_ARG, CUDA. */
+sym_status_t sym_adamw_step(sym_adamw_t a, double lr, double beta1, double beta2, double eps,
+                            double weight_decay, uint64_t step, const float* grad_scale, uint32_t seed,
+                            sym_stream_t stream);
+
+/* out[0] = norm of all the handle's gradients, out[1] = min(1, max_norm /
+ * (norm + 1e-6)), the grad_scale that clips them (NaN, which skips the step,
+ * if the norm is not finite).  out: two device floats.  max_norm > 0.
+ * Deterministic.  Errors: INVALID_ARG, CUDA. */
+sym_status_t sym_grad_norm(sym_adamw_t a, float max_norm, float* out, sym_stream_t stream);
+
+/* Free a handle (not the tensors) after the work that uses it has ended. */
+sym_status_t sym_adamw_free(sym_adamw_t a);
 
 /* ---------------------------------------------------------------- status */
 

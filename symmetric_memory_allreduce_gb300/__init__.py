@@ -1,5 +1,6 @@
 """Symmetric-window collectives on one GB300: AllReduce(sum), AllGather and
-chunked put+signal over R rank windows carved from one GPU's HBM.
+chunked put+signal over R rank windows carved from one GPU's HBM; and the training
+step's operators around that AllReduce (linear layer, policy loss, AdamW).
 
 The compute path is libsymar.so (hand-written CUDA for sm_103a behind the C ABI
 in include/symar.h); this package is its thin ctypes binding.
@@ -12,6 +13,11 @@ from ._binding import (  # noqa: F401
     sym_allreduce_noalloc, sym_signal, sym_signal_read, sym_signal_reset, sym_signal_wait,
     sym_status_string,
     sym_stream_status,
+    ACTS, SYM_ACT_GELU, SYM_ACT_NONE, SYM_ACT_RELU, SYM_ACT_SILU,
     SYM_WINDOW_CUDA_MALLOC, SYM_WINDOW_REGISTERED, SYM_WINDOW_VMM, SYM_WINDOW_VMM_EXPORTABLE,
 )
 from ._binding import LIB_PATH  # noqa: F401
+from ._training import (  # noqa: F401
+    AdamW, sym_adamw_step, sym_grad_norm, sym_linear, sym_linear_backward, sym_policy_loss,
+    sym_policy_loss_backward,
+)

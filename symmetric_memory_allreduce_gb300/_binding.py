@@ -26,6 +26,7 @@ SYM_ALGO_AUTO, SYM_ALGO_ONESHOT, SYM_ALGO_TWOSHOT, SYM_ALGO_PUT_SIGNAL = 0, 1, 2
 SYM_ALGO_TWOSHOT_PULL, SYM_ALGO_TWOSHOT_SPLIT = 4, 5
 SYM_ALGO_COPY, SYM_ALGO_CE = 6, 7
 SYM_WINDOW_CUDA_MALLOC, SYM_WINDOW_REGISTERED, SYM_WINDOW_VMM_EXPORTABLE, SYM_WINDOW_VMM = 0, 1, 2, 3
+SYM_ACT_NONE, SYM_ACT_RELU, SYM_ACT_GELU, SYM_ACT_SILU = 0, 1, 2, 3
 NO_ID = 0xFFFFFFFF
 
 ALGOS = {"auto": SYM_ALGO_AUTO, "oneshot": SYM_ALGO_ONESHOT, "twoshot": SYM_ALGO_TWOSHOT,
@@ -33,6 +34,7 @@ ALGOS = {"auto": SYM_ALGO_AUTO, "oneshot": SYM_ALGO_ONESHOT, "twoshot": SYM_ALGO
          "copy": SYM_ALGO_COPY, "put_signal": SYM_ALGO_PUT_SIGNAL, "ce": SYM_ALGO_CE}
 DTYPES = {"f32": SYM_F32, "bf16": SYM_BF16, "f16": SYM_F16}
 OPS = {"sum": SYM_SUM, "max": SYM_MAX, "min": SYM_MIN}
+ACTS = {"none": SYM_ACT_NONE, "relu": SYM_ACT_RELU, "gelu": SYM_ACT_GELU, "silu": SYM_ACT_SILU}
 
 
 class SymError(RuntimeError):
@@ -46,6 +48,7 @@ _lib = None
 _lock = threading.Lock()
 
 P, sz, i32, u32, u64 = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int, ctypes.c_uint32, ctypes.c_uint64
+f32, f64 = ctypes.c_float, ctypes.c_double
 PP = ctypes.POINTER(ctypes.c_void_p)
 _SIGS = {
     "sym_window_alloc": ([i32, sz, u32, u32, PP], i32),
@@ -77,6 +80,17 @@ _SIGS = {
     "sym_counter_read": ([P, i32, u32, i32, ctypes.POINTER(u64), P], i32),
     "sym_counter_wait": ([P, i32, u32, u64, i32, u64, P], i32),
     "sym_counter_reset": ([P, i32, u32, P], i32),
+    "sym_linear_workspace": ([P, sz, P, sz, sz, sz, sz, i32], sz),
+    "sym_linear": ([P, sz, P, sz, P, P, sz, P, sz, P, sz, sz, sz, sz, i32, i32, P, sz, P], i32),
+    "sym_linear_backward_workspace": ([sz, sz, sz, i32, i32], sz),
+    "sym_linear_backward": ([P, sz, P, sz, P, sz, P, sz, P, sz, P, sz, P, sz, sz, sz, i32, i32, i32, i32, P, sz,
+                             P], i32),
+    "sym_policy_loss": ([P, sz, sz, sz, i32, P, P, P, P, P, f64, f64, f64, f64, P, P, P, P, sz, P, P], i32),
+    "sym_policy_loss_backward": ([P, sz, sz, sz, i32, P, P, P, P, P, f64, f64, f64, f64, P, P, P, sz, P, P], i32),
+    "sym_adamw_create": ([sz, P, P, P, P, P, P, P, P, i32, i32, i32, PP], i32),
+    "sym_adamw_step": ([P, f64, f64, f64, f64, f64, u64, P, u32, P], i32),
+    "sym_grad_norm": ([P, f32, P, P], i32),
+    "sym_adamw_free": ([P], i32),
     "sym_stream_status": ([P], i32),
     "sym_status_string": ([i32], ctypes.c_char_p),
     "sym_last_error": ([], ctypes.c_char_p),

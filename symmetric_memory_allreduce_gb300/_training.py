@@ -1,0 +1,253 @@
+"""ctypes binding of the training step's operators (include/symar.h) -- argument
+marshalling only: sizes, strides and types come from the torch tensors passed in,
+and what the C entry points cannot see of a tensor (its device, the stride within a
+row, its shape) is checked here.  Outputs are the caller's tensors.
+"""
+from __future__ import annotations
+
+import ctypes
+
+from . import _binding as _b
+from ._binding import ACTS, SymError, _check, _stream
+
+_TYPES = {}
+
+
+def _type(t) -> int:
+    """SYM_* code of a tensor's dtype."""
+    if not _TYPES:
+        import torch
+
+        _TYPES.update({torch.float32: _b.SYM_F32, torch.bfloat16: _b.SYM_BF16, torch.float16: _b.SYM_F16})
+    try:
+        return _TYPES[t.dtype]
+    except KeyError:
+        raise ValueError(f"unsupported dtype {t.dtype}") from None
+
+
+def _matrix(t, name, rows, cols, dtype):
+    """(address, row stride) of a rows x cols CUDA tensor with contiguous rows; (None, cols) of None."""
+    if t is None:
+        return None, cols
+    if not t.is_cuda or t.dtype != dtype or t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+        raise ValueError(f"{name}: expected a CUDA {dtype} tensor of shape ({rows}, {cols})")
+    si, sj = t.stride()
+    if cols > 1 and sj != 1:
+        raise ValueError(f"{name}: the elements of a row must be contiguous")
+    if rows > 1 and si < cols:
+        raise ValueError(f"{name}: rows overlap")
+    return t.data_ptr(), (si if rows > 1 else max(cols, 1))
+
+
+def _vector(t, name, n, dtype):
+    """Address of a contiguous CUDA tensor of n elements; None of None."""
+    if t is None:
+        return None
+    if not t.is_cuda or t.dtype != dtype or t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous CUDA {dtype} tensor of {n} elements")
+    return t.data_ptr()
+
+
+def _on_one_device(first, *others):
+    d = first.device
+    for t in others:
+        if t is not None and t.device != d:
+            raise ValueError("tensors on different devices")
+    import torch
+
+    if torch.cuda.current_device() != d.index:
+        raise ValueError(f"the tensors' device {d} is not the current one")
+
+
+def _workspace(given, nbytes, like, stream):
+    """(address, bytes) of the caller's workspace, or of one from torch's allocator on `stream`."""
+    if nbytes == 0:
+        return None, 0
+    import torch
+
+    if given is None:
+        given = torch.empty(nbytes, dtype=torch.uint8, device=like.device)
+        if stream is not None:
+            # freed on return: the allocator must not hand it out before `stream` is through with it
+            given.record_stream(stream if not isinstance(stream, int) else torch.cuda.ExternalStream(stream))
+    elif not given.is_cuda or given.device != like.device or not given.is_contiguous():
+        raise ValueError("workspace: expected a contiguous tensor on the inputs' device")
+    return given.data_ptr(), given.numel() * given.element_size()
+
+
+def sym_linear(x, w, y, bias=None, residual=None, pre=None, act="none", workspace=None, stream=None):
+    """y = act(x w^T + bias) + residual; `pre`, if given, receives x w^T + bias.
+
+    x (M, K), w (N, K), y, residual, pre (M, N), bias (N): CUDA tensors of one dtype (float32,
+    bfloat16, float16) whose rows are contiguous (any row stride).  act: none, relu, gelu, silu."""
+    lib = _b.load()
+    (M, K), N, dt = x.shape, w.shape[0], x.dtype
+    code = _type(x)
+    _on_one_device(x, w, y, bias, residual, pre)
+    px, ldx = _matrix(x, "x", M, K, dt)
+    pw, ldw = _matrix(w, "w", N, K, dt)
+    py, ldy = _matrix(y, "y", M, N, dt)
+    pr, ldr = _matrix(residual, "residual", M, N, dt)
+    pp, ldp = _matrix(pre, "pre", M, N, dt)
+    need = lib.sym_linear_workspace(px, ldx, pw, ldw, M, N, K, code)
+    ws, wsb = _workspace(workspace, need, x, stream)
+    _check(lib.sym_linear(px, ldx, pw, ldw, _vector(bias, "bias", N, dt), pr, ldr, py, ldy, pp, ldp, M, N, K, code,
+                          ACTS.get(act, act), ws, wsb, _stream(stream)), "sym_linear")
+
+
+def sym_linear_backward(dy, x, w, pre=None, dx=None, dw=None, dbias=None, act="none", accumulate=False,
+                        workspace=None, stream=None):
+    """Gradients of sym_linear: dz = dy act'(pre); dx = dz w, dw = dz^T x, dbias = sum of dz's rows.
+
+    dw and dbias are of x's dtype or both float32 (e.g. a view of a rank's window), and are added
+    to when `accumulate`; any of dx, dw, dbias may be None.  The residual's gradient is dy."""
+    import torch
+
+    lib = _b.load()
+    (M, K), N, dt = x.shape, w.shape[0], x.dtype
+    code = _type(x)
+    _on_one_device(x, dy, w, pre, dx, dw, dbias)
+    gt = dw.dtype if dw is not None else dbias.dtype if dbias is not None else dt
+    if gt != dt and gt != torch.float32:
+        raise ValueError("dw and dbias: expected x's dtype or float32")
+    gcode = _TYPES[gt]
+    pdy, lddy = _matrix(dy, "dy", M, N, dt)
+    px, ldx = _matrix(x, "x", M, K, dt)
+    pw, ldw = _matrix(w, "w", N, K, dt)
+    pp, ldp = _matrix(pre, "pre", M, N, dt)
+    pdx, lddx = _matrix(dx, "dx", M, K, dt)
+    pdw, lddw = _matrix(dw, "dw", N, K, gt)
+    a = ACTS.get(act, act)
+    need = lib.sym_linear_backward_workspace(M, N, K, code, a)
+    ws, wsb = _workspace(workspace, need, x, stream)
+    _check(lib.sym_linear_backward(pdy, lddy, px, ldx, pw, ldw, pp, ldp, pdx, lddx, pdw, lddw,
+                                   _vector(dbias, "dbias", N, gt), M, N, K, code, gcode, a, int(bool(accumulate)),
+                                   ws, wsb, _stream(stream)), "sym_linear_backward")
+
+
+def _policy_args(logits, targets, old_logp, ref_logp, advantages, weights):
+    import torch
+
+    T, V = logits.shape
+    f = torch.float32
+    _on_one_device(logits, targets, old_logp, ref_logp, advantages, weights)
+    p, ld = _matrix(logits, "logits", T, V, logits.dtype)
+    return T, V, f, (p, ld, T, V, _type(logits), _vector(targets, "targets", T, torch.int64),
+                     _vector(old_logp, "old_logp", T, f), _vector(ref_logp, "ref_logp", T, f),
+                     _vector(advantages, "advantages", T, f), _vector(weights, "weights", T, f))
+
+
+def sym_policy_loss(logits, targets, old_logp, advantages, weights, stats, logp, lse, ref_logp=None, dlogits=None,
+                    clip_low=0.2, clip_high=0.2, kl_coef=0.0, temperature=1.0, grad_out=None, stream=None):
+    """Clipped policy loss with a KL term over the rows of `logits` (T, V).
+
+    targets (T) int64; old_logp, advantages, weights, ref_logp (T) float32 (weights and ref_logp may
+    be None); outputs stats (4), logp (T), lse (T) float32, and with `dlogits` (T, V) the gradient in
+    the same pass (it may be `logits` itself), times the device scalar `grad_out` if given."""
+    lib = _b.load()
+    T, V, f, head = _policy_args(logits, targets, old_logp, ref_logp, advantages, weights)
+    _on_one_device(logits, stats, logp, lse, dlogits, grad_out)
+    pd, ldd = _matrix(dlogits, "dlogits", T, V, logits.dtype)
+    _check(lib.sym_policy_loss(*head, clip_low, clip_high, kl_coef, temperature, _vector(stats, "stats", 4, f),
+                               _vector(logp, "logp", T, f), _vector(lse, "lse", T, f), pd, ldd,
+                               _vector(grad_out, "grad_out", 1, f), _stream(stream)), "sym_policy_loss")
+
+
+def sym_policy_loss_backward(logits, targets, old_logp, advantages, weights, logp, lse, dlogits, ref_logp=None,
+                             clip_low=0.2, clip_high=0.2, kl_coef=0.0, temperature=1.0, grad_out=None, stream=None):
+    """dlogits from the logp and lse that sym_policy_loss left, with the same other arguments."""
+    lib = _b.load()
+    T, V, f, head = _policy_args(logits, targets, old_logp, ref_logp, advantages, weights)
+    _on_one_device(logits, logp, lse, dlogits, grad_out)
+    pd, ldd = _matrix(dlogits, "dlogits", T, V, logits.dtype)
+    _check(lib.sym_policy_loss_backward(*head, clip_low, clip_high, kl_coef, temperature,
+                                        _vector(logp, "logp", T, f), _vector(lse, "lse", T, f), pd, ldd,
+                                        _vector(grad_out, "grad_out", 1, f), _stream(stream)),
+           "sym_policy_loss_backward")
+
+
+class AdamW:
+    """The tensors an AdamW step goes over (sym_adamw_create): lists of contiguous CUDA tensors.
+
+    params and grads have one dtype each; m and v are float32, or uint8 with m_scales and v_scales
+    (uint8, one per 32 elements) for 8-bit states; copies, if given, receive the new parameters.  The
+    tensors are kept alive by this object and must not move (views of a window's memory do not)."""
+
+    def __init__(self, params, grads, m, v, m_scales=None, v_scales=None, copies=None):
+        import torch
+
+        lib = _b.load()
+        self.handle = None
+        n = len(params)
+        mx8 = m_scales is not None
+        if mx8 != (v_scales is not None):
+            raise ValueError("m_scales and v_scales go together")
+        lists = [("grads", grads), ("m", m), ("v", v)]
+        lists += [("m_scales", m_scales), ("v_scales", v_scales)] if mx8 else []
+        lists += [("copies", copies)] if copies is not None else []
+        for name, ts in lists:
+            if len(ts) != n:
+                raise ValueError(f"{name}: expected {n} tensors")
+        state = torch.uint8 if mx8 else torch.float32
+        counts = [p.numel() for p in params]
+        blocks = [-(-c // 32) for c in counts]
+        pt = params[0].dtype if n else torch.float32
+        gt = grads[0].dtype if n else torch.float32
+        ct = copies[0].dtype if copies else torch.float32
+        for t in (params[:1] + grads[:1] + (copies or [])[:1]):
+            _type(t)
+        if n:
+            _on_one_device(params[0], *[t for _, ts in [("", params)] + lists for t in ts])
+
+        def addresses(name, ts, sizes, dtype):
+            return (ctypes.c_void_p * max(n, 1))(*[_vector(t, f"{name}[{i}]", sizes[i], dtype)
+                                                   for i, t in enumerate(ts)])
+
+        out = ctypes.c_void_p()
+        _check(lib.sym_adamw_create(
+            n, (ctypes.c_size_t * max(n, 1))(*counts), addresses("params", params, counts, pt),
+            addresses("grads", grads, counts, gt), addresses("m", m, counts, state),
+            addresses("v", v, counts, state),
+            addresses("m_scales", m_scales, blocks, torch.uint8) if mx8 else None,
+            addresses("v_scales", v_scales, blocks, torch.uint8) if mx8 else None,
+            addresses("copies", copies, counts, ct) if copies is not None else None,
+            _TYPES.get(pt, 0), _TYPES.get(gt, 0), _TYPES.get(ct, 0), ctypes.byref(out)), "sym_adamw_create")
+        self.handle = out.value
+        self._keepalive = (params, grads, m, v, m_scales, v_scales, copies)
+
+    def free(self):
+        if self.handle:
+            h, self.handle = self.handle, None
+            _check(_b._lib.sym_adamw_free(h), "sym_adamw_free")
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        self.free()
+
+    def __del__(self):
+        try:
+            self.free()
+        except (SymError, TypeError, AttributeError):    # interpreter shutdown
+            pass
+
+
+def sym_adamw_step(plan, lr, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.0, step=1, grad_scale=None, seed=0,
+                   stream=None):
+    """One step in place; grad_scale: a device float32 scalar (sym_grad_norm's second output, say)."""
+    gs = None
+    if grad_scale is not None:
+        import torch
+
+        gs = _vector(grad_scale, "grad_scale", 1, torch.float32)
+    _check(_b.load().sym_adamw_step(plan.handle, lr, beta1, beta2, eps, weight_decay, step, gs, seed & 0xFFFFFFFF,
+                                    _stream(stream)), "sym_adamw_step")
+
+
+def sym_grad_norm(plan, out, max_norm, stream=None):
+    """out (2 float32): the norm of all gradients, and the factor that clips them to max_norm."""
+    import torch
+
+    _check(_b.load().sym_grad_norm(plan.handle, max_norm, _vector(out, "out", 2, torch.float32), _stream(stream)),
+           "sym_grad_norm")

@@ -1,0 +1,429 @@
+// AdamW over many tensors in one launch, and the global norm of their gradients.
+//
+// With g = scale * grad and t = step, every operation rounded once in binary32
+// in this order (so the result is the same bits whatever the launch shape):
+//   m  = m*b1 + g*(1-b1)          v = v*b2 + (g*g)*(1-b2)        r = sqrt(v)
+//   p' = p*(1 - lr*wd) - (m / (r * 1/sqrt(1-b2^t) + eps)) * (lr/(1-b1^t))
+// The step is a stream: it cannot do without reading p, g, m, v and writing
+// p, m, v once.
+//
+// 8-bit states: elements are e4m3, and each 32 consecutive elements of a
+// tensor share one power-of-two scale 2^(s-127), chosen so that the block's
+// largest magnitude lies in (224, 448]; scaling by it is exact.  m is rounded
+// to nearest even.  Of v its root r is stored, since 8 bits hold the root over
+// twice the octaves.  Near its fixed point a step changes r by less than half
+// of an e4m3 step, which rounding to nearest would undo for ever; r is
+// therefore rounded to the step above with the probability of its nearness,
+// by 20 bits mixed from (seed, element index): reproducible, with no state.
+// A root above zero is never stored as zero (it would turn the next m/r into
+// m/eps).  The update itself uses m and v before they are rounded.
+#include <cmath>
+#include <new>
+#include <vector>
+
+#include <cuda_fp8.h>
+
+#include "training.cuh"
+
+namespace symar {
+
+struct AdamTensor {
+    void* p;
+    const void* g;
+    void* m;
+    void* v;
+    uint8_t* ms;
+    uint8_t* vs;
+    void* copy;
+    uint64_t n;
+    uint32_t base;         // global index of element 0 (multiple of 32), low 32 bits
+    int phase;             // element offset of all pointers from a vector boundary; -1: elementwise
+};
+
+struct AdamChunk {
+    uint32_t tensor, index;
+};
+
+constexpr int kAdamThreads = 256;
+constexpr int kAdamVec = 8;                                     // elements per thread
+constexpr size_t kAdamChunk = (size_t)kAdamThreads * kAdamVec;  // elements per block
+constexpr int kNormGroupMax = 32;                               // chunks per block of the norm
+
+}  // namespace symar
+
+struct sym_adamw {
+    int device;
+    sym_dtype_t pt, gt, ct;
+    bool mx8, has_copy;
+    uint32_t nchunks, norm_blocks, norm_group;
+    uint64_t total;
+    void* mem;                        // one allocation: tensors, chunks, partials, counter
+    symar::AdamTensor* tensors;
+    symar::AdamChunk* chunks;
+    float* partial;
+    uint32_t* counter;
+};
+
+namespace symar {
+
+struct AdamArgs {
+    const AdamTensor* tensors;
+    const AdamChunk* chunks;
+    const float* gscale;      // device, or null (1)
+    float b1, b1c, b2, b2c;   // beta and 1 - beta
+    float decay, rcorr, eps, step;
+    uint32_t seed;
+    int ct;                   // type of the copy
+};
+
+__device__ __forceinline__ uint32_t mix32(uint32_t x) {
+    x ^= x >> 16;
+    x *= 0x7FEB352Du;
+    x ^= x >> 15;
+    x *= 0x846CA68Bu;
+    return x ^ (x >> 16);
+}
+
+// Exponent of the block scale for a largest magnitude `amax`: the power of two
+// that brings it into (224, 448].
+__device__ __forceinline__ int block_exponent(float amax) {
+    const int e = (int)((__float_as_uint(amax) + 0x1FFFFFu) >> 23) - 135;
+    return min(max(e, -127), 127);
+}
+
+// 2^e for -127 <= e <= 127 (2^-127 is subnormal).
+__device__ __forceinline__ float pow2i(int e) {
+    return __uint_as_float(e == -127 ? 0x00400000u : (uint32_t)(e + 127) << 23);
+}
+
+__device__ __forceinline__ uint8_t e4m3_nearest(float x) {
+    if (!(fabsf(x) <= 448.f)) return 0x7F;                  // not finite before scaling
+    return (uint8_t)__nv_cvt_float_to_fp8(x, __NV_SATFINITE, __NV_E4M3);
+}
+
+// y >= 0: the code below y plus one with the probability of y's distance from it.
+__device__ __forceinline__ uint8_t e4m3_stochastic(float y, uint32_t h) {
+    if (!(y <= 448.f)) return 0x7F;
+    const int e = max((int)(__float_as_uint(y) >> 23) - 127, -6);
+    const float u = __fmul_rn((float)(h >> 12), 0x1p-20f);
+    int k = (int)floorf(__fadd_rn(__fmul_rn(y, pow2i(3 - e)), u));
+    if (k == 0 && y > 0.f) k = 1;
+    return (uint8_t)((e + 6) * 8 + k);
+}
+
+__device__ __forceinline__ float e4m3_value(uint8_t c) {
+    const __half_raw h = __nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)c, __NV_E4M3);
+    return __half2float(__half(h));
+}
+
+// One element's update; r is the new root of v.
+__device__ __forceinline__ void adam_update(const AdamArgs& a, float gs, float& p, float g, float& m, float& v,
+                                            float& r) {
+    g = __fmul_rn(g, gs);
+    m = __fadd_rn(__fmul_rn(m, a.b1), __fmul_rn(g, a.b1c));
+    v = __fadd_rn(__fmul_rn(v, a.b2), __fmul_rn(__fmul_rn(g, g), a.b2c));
+    r = __fsqrt_rn(v);
+    const float d = __fadd_rn(__fmul_rn(r, a.rcorr), a.eps);
+    p = __fsub_rn(__fmul_rn(p, a.decay), __fmul_rn(__fdiv_rn(m, d), a.step));
+}
+
+__device__ __forceinline__ void store_copy(void* dst, int ct, size_t i, float p) {
+    if (ct == SYM_BF16) static_cast<__nv_bfloat16*>(dst)[i] = __float2bfloat16_rn(p);
+    else if (ct == SYM_F16) static_cast<__half*>(dst)[i] = __float2half_rn(p);
+    else static_cast<float*>(dst)[i] = p;
+}
+
+// Elementwise path of a chunk: thread t takes elements t, t + 256, ... of it, so a warp
+// always holds one whole scale block.  For pointers that share no vector boundary.
+template <class P, class G, bool MX8>
+__device__ __noinline__ void adam_chunk_scalar(const AdamArgs& a, const AdamTensor& T, uint64_t c0, float gs) {
+    for (int k = 0; k < kAdamVec; ++k) {
+        const uint64_t i = c0 + (uint64_t)k * kAdamThreads + threadIdx.x;
+        const bool ok = i < T.n;
+        float p = 0.f, m = 0.f, v = 0.f, r = 0.f;
+        if (ok) {
+            p = load_f<P>(T.p, i);
+            const float g = load_f<G>(T.g, i);
+            if (MX8) {
+                m = __fmul_rn(e4m3_value(static_cast<uint8_t*>(T.m)[i]), pow2i((int)T.ms[i >> 5] - 127));
+                r = __fmul_rn(e4m3_value(static_cast<uint8_t*>(T.v)[i]), pow2i((int)T.vs[i >> 5] - 127));
+                v = __fmul_rn(r, r);
+            } else {
+                m = static_cast<float*>(T.m)[i];
+                v = static_cast<float*>(T.v)[i];
+            }
+            adam_update(a, gs, p, g, m, v, r);
+            store_f<P>(T.p, i, p);
+            if (T.copy) store_copy(T.copy, a.ct, i, p);
+        }
+        if (MX8) {
+            const float am = warp_max(fabsf(m)), ar = warp_max(r);
+            const int em = block_exponent(am), er = block_exponent(ar);
+            if (ok) {
+                static_cast<uint8_t*>(T.m)[i] = e4m3_nearest(__fmul_rn(m, pow2i(-em)));
+                const uint32_t h = mix32(((uint32_t)i + T.base) * 0x9E3779B1u + a.seed);
+                static_cast<uint8_t*>(T.v)[i] = e4m3_stochastic(__fmul_rn(r, pow2i(-er)), h);
+                if ((threadIdx.x & 31) == 0) {
+                    T.ms[i >> 5] = (uint8_t)(em + 127);
+                    T.vs[i >> 5] = (uint8_t)(er + 127);
+                }
+            }
+        } else if (ok) {
+            static_cast<float*>(T.m)[i] = m;
+            static_cast<float*>(T.v)[i] = v;
+        }
+    }
+}
+
+template <class P, class G, bool MX8>
+__global__ void __launch_bounds__(kAdamThreads) k_adamw(AdamArgs a) {
+    const float gs = a.gscale ? __ldg(a.gscale) : 1.f;
+    if (!isfinite(gs)) return;                       // the step is skipped as a whole
+    const AdamChunk c = a.chunks[blockIdx.x];
+    const AdamTensor T = a.tensors[c.tensor];
+    const uint64_t c0 = (uint64_t)c.index * kAdamChunk;
+    adam_chunk_scalar<P, G, MX8>(a, T, c0, gs);
+}
+
+// ---------------------------------------------------------------- gradient norm
+
+// norm = sqrt(sum g^2): each block sums a fixed group of chunks, the last block to
+// finish adds the blocks' sums in index order, so the result does not depend on timing.
+template <class G>
+__global__ void __launch_bounds__(kAdamThreads)
+    k_grad_norm(const AdamTensor* tensors, const AdamChunk* chunks, uint32_t nchunks, uint32_t group, float* partial,
+                uint32_t* counter, float max_norm, float* out) {
+    float s = 0.f;
+    const uint32_t k0 = blockIdx.x * group, k1 = min(k0 + group, nchunks);
+    for (uint32_t k = k0; k < k1; ++k) {
+        const AdamChunk c = chunks[k];
+        const AdamTensor& T = tensors[c.tensor];
+        const uint64_t c0 = (uint64_t)c.index * kAdamChunk, c1 = min(c0 + kAdamChunk, T.n);
+        for (uint64_t i = c0 + threadIdx.x; i < c1; i += kAdamThreads) {
+            const float g = load_f<G>(T.g, i);
+            s = fmaf(g, g, s);
+        }
+    }
+    __shared__ double red[kAdamThreads / 32];
+    __shared__ bool last;
+    double d = block_sum<kAdamThreads>((double)s, red);
+    if (threadIdx.x == 0) {
+        partial[blockIdx.x] = (float)d;
+        __threadfence();
+        last = atomicAdd(counter, 1u) == gridDim.x - 1;
+    }
+    __syncthreads();
+    if (!last) return;
+    __threadfence();
+    double t = 0.;
+    for (uint32_t i = threadIdx.x; i < gridDim.x; i += kAdamThreads) t += (double)__ldcg(partial + i);
+    t = block_sum<kAdamThreads>(t, red);
+    if (threadIdx.x == 0) {
+        *counter = 0;
+        const float norm = (float)sqrt(t);
+        out[0] = norm;
+        out[1] = isfinite(norm) ? fminf(1.f, __fdiv_rn(max_norm, __fadd_rn(norm, 1e-6f))) : nanf("");
+    }
+}
+
+template <class P, class G>
+static const void* adam_kernel2(bool mx8) {
+    return mx8 ? (const void*)k_adamw<P, G, true> : (const void*)k_adamw<P, G, false>;
+}
+
+template <class P>
+static const void* adam_kernel1(sym_dtype_t gt, bool mx8) {
+    switch (gt) {
+        case SYM_F32: return adam_kernel2<P, float>(mx8);
+        case SYM_BF16: return adam_kernel2<P, __nv_bfloat16>(mx8);
+        case SYM_F16: return adam_kernel2<P, __half>(mx8);
+    }
+    return nullptr;
+}
+
+static const void* adam_kernel(sym_dtype_t pt, sym_dtype_t gt, bool mx8) {
+    switch (pt) {
+        case SYM_F32: return adam_kernel1<float>(gt, mx8);
+        case SYM_BF16: return adam_kernel1<__nv_bfloat16>(gt, mx8);
+        case SYM_F16: return adam_kernel1<__half>(gt, mx8);
+    }
+    return nullptr;
+}
+
+// Offset in elements of `ptr` from a boundary of kAdamVec elements of `es` bytes.
+static int phase_of(const void* ptr, size_t es) { return (int)(((uintptr_t)ptr / es) % kAdamVec); }
+
+}  // namespace symar
+
+using namespace symar;
+
+extern "C" {
+
+sym_status_t sym_adamw_create(size_t ntensors, const size_t* counts, void* const* params, const void* const* grads,
+                              void* const* exp_avg, void* const* exp_avg_sq, void* const* exp_avg_scale,
+                              void* const* exp_avg_sq_scale, void* const* copies, sym_dtype_t param_dtype,
+                              sym_dtype_t grad_dtype, sym_dtype_t copy_dtype, sym_adamw_t* out) {
+    if (out) *out = nullptr;
+    if (!out || (ntensors && (!counts || !params || !grads || !exp_avg || !exp_avg_sq))) return SYM_ERR_INVALID_ARG;
+    const size_t ps = dtype_size(param_dtype), gs = dtype_size(grad_dtype), cs = dtype_size(copy_dtype);
+    if (!ps || !gs || !cs) return SYM_ERR_INVALID_ARG;
+    if ((exp_avg_scale == nullptr) != (exp_avg_sq_scale == nullptr)) return SYM_ERR_INVALID_ARG;
+    const bool mx8 = exp_avg_scale != nullptr;
+    if (ntensors >= (1u << 31)) return SYM_ERR_UNSUPPORTED;
+    // C++ exceptions end here: the caller may be plain C
+    try {
+        std::vector<AdamTensor> ts;
+        std::vector<AdamChunk> cks;
+        uint64_t base = 0, total = 0;
+        for (size_t i = 0; i < ntensors; ++i) {
+            const size_t n = counts[i];
+            if (n == 0) continue;
+            if (n > ((size_t)1 << 42)) return SYM_ERR_UNSUPPORTED;
+            AdamTensor t{};
+            t.p = params[i];
+            t.g = grads[i];
+            t.m = exp_avg[i];
+            t.v = exp_avg_sq[i];
+            t.ms = mx8 ? (uint8_t*)exp_avg_scale[i] : nullptr;
+            t.vs = mx8 ? (uint8_t*)exp_avg_sq_scale[i] : nullptr;
+            t.copy = copies ? copies[i] : nullptr;
+            if (!t.p || !t.g || !t.m || !t.v || (mx8 && (!t.ms || !t.vs)) || (copies && !t.copy)) {
+                set_last_error("sym_adamw_create: null tensor pointer");
+                return SYM_ERR_INVALID_ARG;
+            }
+            const size_t ss = mx8 ? 1 : 4;
+            if ((uintptr_t)t.p % ps || (uintptr_t)t.g % gs || (uintptr_t)t.m % ss || (uintptr_t)t.v % ss ||
+                (uintptr_t)t.copy % cs) {
+                set_last_error("sym_adamw_create: pointer not aligned to its element type");
+                return SYM_ERR_INVALID_ARG;
+            }
+            t.n = n;
+            t.base = (uint32_t)base;
+            const int ph = phase_of(t.p, ps);
+            const bool same = ph == phase_of(t.g, gs) && ph == phase_of(t.m, ss) && ph == phase_of(t.v, ss) &&
+                              (!t.copy || ph == phase_of(t.copy, cs));
+            t.phase = same && !(mx8 && ph) ? ph : -1;
+            const size_t span = n + (t.phase > 0 ? t.phase : 0);
+            for (size_t k = 0; k < ceil_div(span, kAdamChunk); ++k) cks.push_back({(uint32_t)ts.size(), (uint32_t)k});
+            if (cks.size() >= (1u << 31)) return SYM_ERR_UNSUPPORTED;
+            ts.push_back(t);
+            base += ceil_div(n, (size_t)32) * 32;
+            total += n;
+        }
+        int dev = 0;
+        SYM_CUDA(cudaGetDevice(&dev));
+        DevCtx* ctx = dev_ctx(dev);
+        if (!ctx) return SYM_ERR_CUDA;
+        sym_adamw* a = new sym_adamw();
+        a->device = dev;
+        a->pt = param_dtype;
+        a->gt = grad_dtype;
+        a->ct = copy_dtype;
+        a->mx8 = mx8;
+        a->has_copy = copies != nullptr;
+        a->nchunks = (uint32_t)cks.size();
+        a->total = total;
+        // the norm's blocks: a few per SM at least, up to 32 chunks each
+        a->norm_group = (uint32_t)std::min<size_t>(std::max<size_t>(cks.size() / (size_t)(ctx->num_sms * 16), 1),
+                                                   kNormGroupMax);
+        a->norm_blocks = (uint32_t)ceil_div(cks.size(), (size_t)a->norm_group);
+        const size_t tb = ceil_div(ts.size() * sizeof(AdamTensor), (size_t)256) * 256;
+        const size_t cb = ceil_div(cks.size() * sizeof(AdamChunk), (size_t)256) * 256;
+        const size_t pb = ceil_div(std::max(a->norm_blocks, 1u) * sizeof(float), (size_t)256) * 256;
+        char* mem = nullptr;
+        cudaError_t e = cudaMalloc(&mem, tb + cb + pb + 256);
+        if (e == cudaSuccess && !ts.empty())
+            e = cudaMemcpy(mem, ts.data(), ts.size() * sizeof(AdamTensor), cudaMemcpyHostToDevice);
+        if (e == cudaSuccess && !cks.empty())
+            e = cudaMemcpy(mem + tb, cks.data(), cks.size() * sizeof(AdamChunk), cudaMemcpyHostToDevice);
+        if (e == cudaSuccess) e = cudaMemset(mem + tb + cb + pb, 0, 256);
+        // the legacy-stream memset above must have ended before a step on a non-blocking stream
+        if (e == cudaSuccess) e = cudaStreamSynchronize(nullptr);
+        if (e != cudaSuccess) {
+            if (mem) cudaFree(mem);
+            delete a;
+            return cuda_fail(e, "sym_adamw_create");
+        }
+        a->mem = mem;
+        a->tensors = (AdamTensor*)mem;
+        a->chunks = (AdamChunk*)(mem + tb);
+        a->partial = (float*)(mem + tb + cb);
+        a->counter = (uint32_t*)(mem + tb + cb + pb);
+        *out = a;
+        return SYM_OK;
+    } catch (const std::bad_alloc&) {
+        set_last_error("sym_adamw_create: out of host memory");
+        return SYM_ERR_OOM;
+    } catch (...) {
+        set_last_error("sym_adamw_create: host error");
+        return SYM_ERR_CUDA;
+    }
+}
+
+sym_status_t sym_adamw_free(sym_adamw_t a) {
+    if (!a) return SYM_OK;
+    DeviceGuard g(a->device);
+    if (!g.ok) return SYM_ERR_CUDA;
+    cudaError_t e = cudaFree(a->mem);
+    delete a;
+    return e == cudaSuccess ? SYM_OK : cuda_fail(e, "cudaFree(adamw)");
+}
+
+sym_status_t sym_adamw_step(sym_adamw_t a, double lr, double beta1, double beta2, double eps, double weight_decay,
+                            uint64_t step, const float* grad_scale, uint32_t seed, sym_stream_t stream) {
+    if (!a || step == 0) return SYM_ERR_INVALID_ARG;
+    if (!(beta1 >= 0 && beta1 < 1 && beta2 >= 0 && beta2 < 1 && eps >= 0) || !std::isfinite(lr) ||
+        !std::isfinite(eps) || !std::isfinite(weight_decay))
+        return SYM_ERR_INVALID_ARG;
+    if ((uintptr_t)grad_scale % sizeof(float)) return SYM_ERR_INVALID_ARG;
+    if (a->nchunks == 0) return SYM_OK;
+    DeviceGuard g(a->device);
+    if (!g.ok) return SYM_ERR_CUDA;
+    AdamArgs k{};
+    k.tensors = a->tensors;
+    k.chunks = a->chunks;
+    k.gscale = grad_scale;
+    k.b1 = (float)beta1;
+    k.b1c = (float)(1.0 - beta1);
+    k.b2 = (float)beta2;
+    k.b2c = (float)(1.0 - beta2);
+    k.decay = (float)(1.0 - lr * weight_decay);
+    k.rcorr = (float)(1.0 / std::sqrt(1.0 - std::pow(beta2, (double)step)));
+    k.eps = (float)eps;
+    k.step = (float)(lr / (1.0 - std::pow(beta1, (double)step)));
+    k.seed = seed;
+    k.ct = (int)a->ct;
+    void* args[] = {&k};
+    SYM_CUDA(cudaLaunchKernel(adam_kernel(a->pt, a->gt, a->mx8), dim3(a->nchunks), dim3(kAdamThreads), args, 0,
+                              (cudaStream_t)stream));
+    count_launch();
+    return SYM_OK;
+}
+
+sym_status_t sym_grad_norm(sym_adamw_t a, float max_norm, float* out, sym_stream_t stream) {
+    if (!a || !out || (uintptr_t)out % sizeof(float) || !(max_norm > 0.f)) return SYM_ERR_INVALID_ARG;
+    DeviceGuard g(a->device);
+    if (!g.ok) return SYM_ERR_CUDA;
+    cudaStream_t st = (cudaStream_t)stream;
+    const unsigned grid = std::max(a->norm_blocks, 1u);    // no elements: one block writes norm 0, scale 1
+    switch (a->gt) {
+        case SYM_F32:
+            k_grad_norm<float><<<grid, kAdamThreads, 0, st>>>(a->tensors, a->chunks, a->nchunks, a->norm_group,
+                                                              a->partial, a->counter, max_norm, out);
+            break;
+        case SYM_BF16:
+            k_grad_norm<__nv_bfloat16><<<grid, kAdamThreads, 0, st>>>(a->tensors, a->chunks, a->nchunks,
+                                                                      a->norm_group, a->partial, a->counter,
+                                                                      max_norm, out);
+            break;
+        case SYM_F16:
+            k_grad_norm<__half><<<grid, kAdamThreads, 0, st>>>(a->tensors, a->chunks, a->nchunks, a->norm_group,
+                                                               a->partial, a->counter, max_norm, out);
+            break;
+    }
+    count_launch();
+    SYM_CUDA(cudaGetLastError());
+    return SYM_OK;
+}
+
+}  // extern "C"

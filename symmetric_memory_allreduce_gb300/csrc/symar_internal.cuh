@@ -33,6 +33,8 @@ enum WaitSite : uint32_t {
     kSiteBulkStage = 5,
     kSiteSignalChain = 6,      // a put waited for the previous batch's signal of its pair
     kSiteBarrier = 7,          // a rank waited at a barrier for the other ranks' signals
+    kSitePolicyTarget = 8,     // policy loss: a row's target is no column of the logits (no wait)
+    kSiteLinearStage = 9,      // linear: an operand tile or an accumulator was not ready in time
 };
 
 // Per-device context: the status block and the arrival ring used by

@@ -1,0 +1,61 @@
+// Device helpers shared by the training operators (linear, policy loss, AdamW).
+#pragma once
+
+#include <algorithm>
+
+#include <cuda_fp16.h>
+
+#include "symar_internal.cuh"
+
+namespace symar {
+
+template <class T>
+__device__ __forceinline__ float to_f(T x);
+template <>
+__device__ __forceinline__ float to_f(float x) { return x; }
+template <>
+__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
+template <>
+__device__ __forceinline__ float to_f(__half x) { return __half2float(x); }
+
+template <class T>
+__device__ __forceinline__ T from_f(float x);
+template <>
+__device__ __forceinline__ float from_f(float x) { return x; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f(float x) { return __float2bfloat16_rn(x); }
+template <>
+__device__ __forceinline__ __half from_f(float x) { return __float2half_rn(x); }
+
+template <class T>
+__device__ __forceinline__ float load_f(const void* p, size_t i) { return to_f(static_cast<const T*>(p)[i]); }
+template <class T>
+__device__ __forceinline__ void store_f(void* p, size_t i, float x) { static_cast<T*>(p)[i] = from_f<T>(x); }
+
+__device__ __forceinline__ float warp_max(float x) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) x = fmaxf(x, __shfl_xor_sync(~0u, x, o));
+    return x;
+}
+
+template <class T>
+__device__ __forceinline__ T warp_sum(T x) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(~0u, x, o);
+    return x;
+}
+
+// Sum over a block in a fixed order; every thread gets it.  red: THREADS/32 slots.
+template <int THREADS, class T>
+__device__ __forceinline__ T block_sum(T x, T* red) {
+    x = warp_sum(x);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = x;
+    __syncthreads();
+    T s = red[0];
+#pragma unroll
+    for (int w = 1; w < THREADS / 32; ++w) s += red[w];
+    return s;
+}
+
+}  // namespace symar
