@@ -421,7 +421,9 @@ sym_status_t sym_linear(const void* x, size_t ldx, const void* w, size_t ldw, co
  * makes dw and dbias 0 (or leaves them, accumulating).  The sums' order does
  * not depend on timing: equal calls give equal bits.
  * Errors: as sym_linear. */
-size_t sym_linear_backward_workspace(size_t M, size_t N, size_t K, sym_dtype_t dtype, sym_act_t act);
+size_t sym_linear_backward_workspace(const void* dy, size_t lddy, const void* x, size_t ldx,
+                                     const void* w, size_t ldw, size_t M, size_t N, size_t K,
+                                     sym_dtype_t dtype, sym_act_t act);
 sym_status_t sym_linear_backward(const void* dy, size_t lddy, const void* x, size_t ldx, const void* w,
                                  size_t ldw, const void* pre, size_t ldp, void* dx, size_t lddx,
                                  void* dw, size_t lddw, void* dbias, size_t M, size_t N, size_t K,

@@ -82,7 +82,7 @@ _SIGS = {
     "sym_counter_reset": ([P, i32, u32, P], i32),
     "sym_linear_workspace": ([P, sz, P, sz, sz, sz, sz, i32], sz),
     "sym_linear": ([P, sz, P, sz, P, P, sz, P, sz, P, sz, sz, sz, sz, i32, i32, P, sz, P], i32),
-    "sym_linear_backward_workspace": ([sz, sz, sz, i32, i32], sz),
+    "sym_linear_backward_workspace": ([P, sz, P, sz, P, sz, sz, sz, sz, i32, i32], sz),
     "sym_linear_backward": ([P, sz, P, sz, P, sz, P, sz, P, sz, P, sz, P, sz, sz, sz, i32, i32, i32, i32, P, sz,
                              P], i32),
     "sym_policy_loss": ([P, sz, sz, sz, i32, P, P, P, P, P, f64, f64, f64, f64, P, P, P, P, sz, P, P], i32),

@@ -118,7 +118,7 @@ def sym_linear_backward(dy, x, w, pre=None, dx=None, dw=None, dbias=None, act="n
     pdx, lddx = _matrix(dx, "dx", M, K, dt)
     pdw, lddw = _matrix(dw, "dw", N, K, gt)
     a = ACTS.get(act, act)
-    need = lib.sym_linear_backward_workspace(M, N, K, code, a)
+    need = lib.sym_linear_backward_workspace(pdy, lddy, px, ldx, pw, ldw, M, N, K, code, a)
     ws, wsb = _workspace(workspace, need, x, stream)
     _check(lib.sym_linear_backward(pdy, lddy, px, ldx, pw, ldw, pp, ldp, pdx, lddx, pdw, lddw,
                                    _vector(dbias, "dbias", N, gt), M, N, K, code, gcode, a, int(bool(accumulate)),

@@ -120,7 +120,7 @@ def test_f32_states_bit_exact(symar, name, params, grads, offset):
                     want = p64 * (1 - 1e-3) - q * m1
                     tol = 16 * 2.0 ** -24 * (np.abs(want) + np.abs(p64) + q * (np.abs(0.9 * m64) + np.abs(0.1 * g64)))
                     u = UNIT[p[i].dtype]
-                    close(p[i].cpu(), torch.from_numpy(want), torch.from_numpy(tol) + u * 1.01 * np.abs(want) + TINY[p[i].dtype], "p")
+                    close(p[i].cpu(), torch.from_numpy(want), torch.from_numpy(tol + u * 1.01 * np.abs(want) + TINY[p[i].dtype]), "p")
                     close(m[i].cpu(), torch.from_numpy(m1), torch.from_numpy(4 * 2.0 ** -24 * (np.abs(0.9 * m64) + np.abs(0.1 * g64))), "m")
                     close(v[i].cpu(), torch.from_numpy(v1), torch.from_numpy(4 * 2.0 ** -24 * np.abs(v1)), "v")
                 a_t = torch.from_numpy(a).to(p[i].dtype)

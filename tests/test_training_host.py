@@ -41,6 +41,12 @@ def test_linear_workspace_covers_unaligned_rows(lib):
     assert f(A, 64, 2 * A, 64, 100, 100, 64, 1) == 0
     assert f(A, 64, 2 * A, 64, 100, 100, 64, 0) == 0
     assert f(A, 64, 2 * A, 64, 0, 100, 64, 1) == 0
+    assert f(A + 2, 64, 2 * A, 64, 100, 50, 64, 1) >= 100 * 64 * 2      # x at an odd element
+    assert f(A, 65, 2 * A, 65, 100, 50, 65, 2) >= (100 + 50) * 72 * 2   # odd rows, both padded to 72
+    assert f(A + 4, 65, 2 * A, 65, 100, 50, 65, 0) == 0
+    assert _linear(lib, ldx=65, ws=None) == 1
+    assert _linear(lib, ldx=65, ws=9 * A + 8, wsb=1 << 20) == 1
+    assert _linear(lib, ldx=65, ws=A + 256, wsb=1 << 20) == 1           # over x
 
 
 def _backward(lib, **kw):
@@ -57,8 +63,9 @@ def test_linear_backward_refusals(lib):
         assert _backward(lib, **kw) == 1, kw
     assert _backward(lib, M=1 << 31) == 5
     assert _backward(lib, dx=None, dw=None, dbias=None) == 0
-    need = lib.sym_linear_backward_workspace
-    assert need(8, 64, 64, 1, 1) >= need(8, 64, 64, 1, 0) >= 64 * 4
+    need = lambda act, ld=64: lib.sym_linear_backward_workspace(A, ld, 2 * A, 64, 3 * A, 64, 8, 64, 64, 1, act)  # noqa: E731
+    assert need(1) >= need(0) + 8 * 64 * 2 and need(0) >= 64 * 4
+    assert need(0, 65) >= need(0) + 8 * 64 * 2 and need(1, 65) == need(1)
     assert lib.sym_launch_count() == 0
 
 
