@@ -38,6 +38,7 @@ struct AdamTensor {
     uint64_t n;
     uint32_t base;         // global index of element 0 (multiple of 32), low 32 bits
     int phase;             // element offset of all pointers from a vector boundary; -1: elementwise
+    int gphase;            // the same of g alone
 };
 
 struct AdamChunk {
@@ -66,15 +67,6 @@ struct sym_adamw {
 
 namespace symar {
 
-struct AdamArgs {
-    const AdamTensor* tensors;
-    const AdamChunk* chunks;
-    const float* gscale;      // device, or null (1)
-    float b1, b1c, b2, b2c;   // beta and 1 - beta
-    float decay, rcorr, eps, step;
-    uint32_t seed;
-    int ct;                   // type of the copy
-};
 
 __device__ __forceinline__ uint32_t mix32(uint32_t x) {
     x ^= x >> 16;
@@ -96,19 +88,58 @@ __device__ __forceinline__ float pow2i(int e) {
     return __uint_as_float(e == -127 ? 0x00400000u : (uint32_t)(e + 127) << 23);
 }
 
+// Two binary32 operations per instruction, each rounded once (no contraction across them).
+struct F2 {
+    uint64_t v;
+};
+__device__ __forceinline__ F2 f2(float x, float y) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ void split(F2 a, float& x, float& y) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(a.v));
+}
+// a*b + z with z = (-0, -0) is a*b rounded once, signs of zero included.  z is a kernel argument: a
+// packed product the compiler can see is contracted with the sum that follows it (measured: other
+// bits than mul and add apart).
+__device__ __forceinline__ F2 mul2(F2 a, F2 b, F2 z) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(z.v));
+    return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+
+struct AdamArgs {
+    const AdamTensor* tensors;
+    const AdamChunk* chunks;
+    const float* gscale;      // device, or null (1)
+    float b1, b1c, b2, b2c;   // beta and 1 - beta
+    float decay, rcorr, eps, step;
+    uint32_t seed;
+    int ct;                   // type of the copy
+    F2 nz;                    // (-0, -0), see mul2
+};
+
 __device__ __forceinline__ uint8_t e4m3_nearest(float x) {
     if (!(fabsf(x) <= 448.f)) return 0x7F;                  // not finite before scaling
     return (uint8_t)__nv_cvt_float_to_fp8(x, __NV_SATFINITE, __NV_E4M3);
 }
 
-// y >= 0: the code below y plus one with the probability of y's distance from it.
-__device__ __forceinline__ uint8_t e4m3_stochastic(float y, uint32_t h) {
-    if (!(y <= 448.f)) return 0x7F;
-    const int e = max((int)(__float_as_uint(y) >> 23) - 127, -6);
-    const float u = __fmul_rn((float)(h >> 12), 0x1p-20f);
-    int k = (int)floorf(__fadd_rn(__fmul_rn(y, pow2i(3 - e)), u));
-    if (k == 0 && y > 0.f) k = 1;
-    return (uint8_t)((e + 6) * 8 + k);
+// y >= 0: the code below y plus one with the probability of y's distance from it, by the upper 20
+// bits of h.  With e = max(exponent of y, -6) the code is 8 (e + 6) + floor(y 2^(3-e) + u), u in [0,1);
+// adding 2^23 rounded down leaves that floor in the low bits.  What is not finite becomes 0x7F (NaN).
+__device__ __forceinline__ uint32_t e4m3_stochastic(float y, uint32_t h) {
+    const uint32_t bits = __float_as_uint(y);
+    const uint32_t eb = max(bits & 0x7F800000u, 121u << 23);
+    const float u = __fadd_rn(__uint_as_float((h >> 9 & ~7u) | 0x3F800000u), -1.f);
+    const float z = __fadd_rn(__fmul_rn(y, __uint_as_float((257u << 23) - eb)), u);
+    const uint32_t code = (eb >> 20) + __float_as_uint(__fadd_rd(z, 0x1p23f)) - (968u + 0x4B000000u);
+    return min(max(code, min(bits, 1u)), 0x7Fu);
 }
 
 __device__ __forceinline__ float e4m3_value(uint8_t c) {
@@ -116,7 +147,30 @@ __device__ __forceinline__ float e4m3_value(uint8_t c) {
     return __half2float(__half(h));
 }
 
-// One element's update; r is the new root of v.
+// The values of the codes in bits 0-7 and 8-15 of c, times a power of two.
+__device__ __forceinline__ void e4m3_values2(uint32_t c, float scale, F2 nz, float* x) {
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)c, __NV_E4M3);
+    const float2 f = __half22float2(__half2(h));
+    split(mul2(f2(f.x, f.y), f2(scale, scale), nz), x[0], x[1]);
+}
+
+// Two elements' update; r receives the new roots of v.
+__device__ __forceinline__ void adam_update2(const AdamArgs& a, float gs, float* p, const float* g, float* m, float* v,
+                                             float* r) {
+    const F2 gg = mul2(f2(g[0], g[1]), f2(gs, gs), a.nz);
+    const F2 mm = add2(mul2(f2(m[0], m[1]), f2(a.b1, a.b1), a.nz), mul2(gg, f2(a.b1c, a.b1c), a.nz));
+    const F2 vv = add2(mul2(f2(v[0], v[1]), f2(a.b2, a.b2), a.nz), mul2(mul2(gg, gg, a.nz), f2(a.b2c, a.b2c), a.nz));
+    split(mm, m[0], m[1]);
+    split(vv, v[0], v[1]);
+    r[0] = __fsqrt_rn(v[0]);
+    r[1] = __fsqrt_rn(v[1]);
+    float d0, d1;
+    split(add2(mul2(f2(r[0], r[1]), f2(a.rcorr, a.rcorr), a.nz), f2(a.eps, a.eps)), d0, d1);
+    const F2 q = f2(__fdiv_rn(m[0], d0), __fdiv_rn(m[1], d1));
+    split(add2(mul2(f2(p[0], p[1]), f2(a.decay, a.decay), a.nz), mul2(q, f2(-a.step, -a.step), a.nz)), p[0], p[1]);
+}
+
+// One element's.
 __device__ __forceinline__ void adam_update(const AdamArgs& a, float gs, float& p, float g, float& m, float& v,
                                             float& r) {
     g = __fmul_rn(g, gs);
@@ -136,7 +190,7 @@ __device__ __forceinline__ void store_copy(void* dst, int ct, size_t i, float p)
 // Elementwise path of a chunk: thread t takes elements t, t + 256, ... of it, so a warp
 // always holds one whole scale block.  For pointers that share no vector boundary.
 template <class P, class G, bool MX8>
-__device__ __noinline__ void adam_chunk_scalar(const AdamArgs& a, const AdamTensor& T, uint64_t c0, float gs) {
+__device__ __forceinline__ void adam_chunk_scalar(const AdamArgs& a, const AdamTensor& T, uint64_t c0, float gs) {
     for (int k = 0; k < kAdamVec; ++k) {
         const uint64_t i = c0 + (uint64_t)k * kAdamThreads + threadIdx.x;
         const bool ok = i < T.n;
@@ -162,7 +216,7 @@ __device__ __noinline__ void adam_chunk_scalar(const AdamArgs& a, const AdamTens
             if (ok) {
                 static_cast<uint8_t*>(T.m)[i] = e4m3_nearest(__fmul_rn(m, pow2i(-em)));
                 const uint32_t h = mix32(((uint32_t)i + T.base) * 0x9E3779B1u + a.seed);
-                static_cast<uint8_t*>(T.v)[i] = e4m3_stochastic(__fmul_rn(r, pow2i(-er)), h);
+                static_cast<uint8_t*>(T.v)[i] = (uint8_t)e4m3_stochastic(__fmul_rn(r, pow2i(-er)), h);
                 if ((threadIdx.x & 31) == 0) {
                     T.ms[i >> 5] = (uint8_t)(em + 127);
                     T.vs[i >> 5] = (uint8_t)(er + 127);
@@ -175,14 +229,160 @@ __device__ __noinline__ void adam_chunk_scalar(const AdamArgs& a, const AdamTens
     }
 }
 
+// Eight neighbouring elements by 16-byte (8-bit codes: 8-byte) accesses.  Every byte is used once:
+// streaming loads and stores, so that they do not displace what the next kernels read from L2.
+template <class T>
+__device__ __forceinline__ void load8(const void* base, uint64_t i, float (&f)[8]) {
+    const uint4* q = reinterpret_cast<const uint4*>(static_cast<const T*>(base) + i);
+    if (sizeof(T) == 4) {
+        const uint4 a = __ldcs(q), b = __ldcs(q + 1);
+        f[0] = __uint_as_float(a.x), f[1] = __uint_as_float(a.y), f[2] = __uint_as_float(a.z), f[3] = __uint_as_float(a.w);
+        f[4] = __uint_as_float(b.x), f[5] = __uint_as_float(b.y), f[6] = __uint_as_float(b.z), f[7] = __uint_as_float(b.w);
+    } else {
+        const uint4 a = __ldcs(q);
+        const T* h = reinterpret_cast<const T*>(&a);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] = to_f(h[e]);
+    }
+}
+
+template <class T>
+__device__ __forceinline__ void store8(void* base, uint64_t i, const float (&f)[8]) {
+    uint4* q = reinterpret_cast<uint4*>(static_cast<T*>(base) + i);
+    if (sizeof(T) == 4) {
+        __stcs(q, make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3])));
+        __stcs(q + 1, make_uint4(__float_as_uint(f[4]), __float_as_uint(f[5]), __float_as_uint(f[6]), __float_as_uint(f[7])));
+    } else {
+        uint4 a;
+        T* h = reinterpret_cast<T*>(&a);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) h[e] = from_f<T>(f[e]);
+        __stcs(q, a);
+    }
+}
+
+__device__ __forceinline__ void store_copy8(void* dst, int ct, uint64_t i, const float (&p)[8]) {
+    if (ct == SYM_BF16) store8<__nv_bfloat16>(dst, i, p);
+    else if (ct == SYM_F16) store8<__half>(dst, i, p);
+    else store8<float>(dst, i, p);
+}
+
+// One block per chunk of 2048 elements, 8 neighbouring ones per thread, counted from the vector
+// boundary at or before the tensor's start; a thread whose eight are not all inside goes one by one.
 template <class P, class G, bool MX8>
 __global__ void __launch_bounds__(kAdamThreads) k_adamw(AdamArgs a) {
     const float gs = a.gscale ? __ldg(a.gscale) : 1.f;
-    if (!isfinite(gs)) return;                       // the step is skipped as a whole
     const AdamChunk c = a.chunks[blockIdx.x];
     const AdamTensor T = a.tensors[c.tensor];
+    if (!isfinite(gs)) return;                       // the step is skipped as a whole
     const uint64_t c0 = (uint64_t)c.index * kAdamChunk;
-    adam_chunk_scalar<P, G, MX8>(a, T, c0, gs);
+    if (T.phase < 0) return adam_chunk_scalar<P, G, MX8>(a, T, c0, gs);
+    const int64_t first = (int64_t)(c0 + threadIdx.x * kAdamVec) - T.phase;
+    const uint64_t i = (uint64_t)first;
+    if (MX8) {
+        // phase 0; four threads hold a scale block, so whole warps stay together
+        uint8_t* cm = static_cast<uint8_t*>(T.m);
+        uint8_t* cv = static_cast<uint8_t*>(T.v);
+        float p[8], g[8], m[8], r[8];
+        float am = 0.f, ar = 0.f;
+        const bool whole = i + 8 <= T.n;
+        if (whole) {
+            const uint2 xm = __ldcs(reinterpret_cast<const uint2*>(cm + i)), xv = __ldcs(reinterpret_cast<const uint2*>(cv + i));
+            const float sm = pow2i((int)T.ms[i >> 5] - 127), sv = pow2i((int)T.vs[i >> 5] - 127);
+            load8<P>(T.p, i, p);
+            load8<G>(T.g, i, g);
+#pragma unroll
+            for (int e = 0; e < 8; e += 2) {
+                e4m3_values2((e < 4 ? xm.x : xm.y) >> (e % 4 * 8), sm, a.nz, m + e);
+                e4m3_values2((e < 4 ? xv.x : xv.y) >> (e % 4 * 8), sv, a.nz, r + e);
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const bool in = i + e < T.n;
+                p[e] = in ? load_f<P>(T.p, i + e) : 0.f;
+                g[e] = in ? load_f<G>(T.g, i + e) : 0.f;
+                m[e] = in ? __fmul_rn(e4m3_value(cm[i + e]), pow2i((int)T.ms[(i + e) >> 5] - 127)) : 0.f;
+                r[e] = in ? __fmul_rn(e4m3_value(cv[i + e]), pow2i((int)T.vs[(i + e) >> 5] - 127)) : 0.f;
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < 8; e += 2) {
+            float v[2];
+            split(mul2(f2(r[e], r[e + 1]), f2(r[e], r[e + 1]), a.nz), v[0], v[1]);
+            adam_update2(a, gs, p + e, g + e, m + e, v, r + e);
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            if (!whole && i + e >= T.n) m[e] = r[e] = 0.f;
+            am = fmaxf(am, fabsf(m[e]));
+            ar = fmaxf(ar, r[e]);
+        }
+#pragma unroll
+        for (int o = 1; o < 4; o <<= 1) {
+            am = fmaxf(am, __shfl_xor_sync(~0u, am, o));
+            ar = fmaxf(ar, __shfl_xor_sync(~0u, ar, o));
+        }
+        const int em = block_exponent(am), er = block_exponent(ar);
+        const float fm = pow2i(-em), fr = pow2i(-er);
+        uint32_t ym[2] = {0, 0}, yv[2] = {0, 0};
+        const uint32_t h0 = ((uint32_t)i + T.base) * 0x9E3779B1u + a.seed;
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            yv[e / 4] |= e4m3_stochastic(__fmul_rn(r[e], fr), mix32(h0 + e * 0x9E3779B1u)) << (e % 4 * 8);
+        if (am <= 3.4e38f) {
+#pragma unroll
+            for (int e = 0; e < 8; e += 2)
+                ym[e / 4] |= (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(__fmul_rn(m[e], fm), __fmul_rn(m[e + 1], fm)),
+                                                                __NV_SATFINITE, __NV_E4M3)
+                             << (e % 4 * 8);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) ym[e / 4] |= (uint32_t)e4m3_nearest(__fmul_rn(m[e], fm)) << (e % 4 * 8);
+        }
+        if (whole) {
+            store8<P>(T.p, i, p);
+            if (T.copy) store_copy8(T.copy, a.ct, i, p);
+            __stcs(reinterpret_cast<uint2*>(cm + i), make_uint2(ym[0], ym[1]));
+            __stcs(reinterpret_cast<uint2*>(cv + i), make_uint2(yv[0], yv[1]));
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                if (i + e >= T.n) break;
+                store_f<P>(T.p, i + e, p[e]);
+                if (T.copy) store_copy(T.copy, a.ct, i + e, p[e]);
+                cm[i + e] = (uint8_t)(ym[e / 4] >> (e % 4 * 8));
+                cv[i + e] = (uint8_t)(yv[e / 4] >> (e % 4 * 8));
+            }
+        }
+        if ((threadIdx.x & 3) == 0 && i < T.n) {
+            T.ms[i >> 5] = (uint8_t)(em + 127);
+            T.vs[i >> 5] = (uint8_t)(er + 127);
+        }
+    } else if (first >= 0 && i + 8 <= T.n) {
+        float p[8], g[8], m[8], v[8], r[2];
+        load8<P>(T.p, i, p);
+        load8<G>(T.g, i, g);
+        load8<float>(T.m, i, m);
+        load8<float>(T.v, i, v);
+#pragma unroll
+        for (int e = 0; e < 8; e += 2) adam_update2(a, gs, p + e, g + e, m + e, v + e, r);
+        store8<P>(T.p, i, p);
+        store8<float>(T.m, i, m);
+        store8<float>(T.v, i, v);
+        if (T.copy) store_copy8(T.copy, a.ct, i, p);
+    } else {
+        for (int e = 0; e < 8; ++e) {
+            const int64_t k = first + e;
+            if (k < 0 || (uint64_t)k >= T.n) continue;
+            float p = load_f<P>(T.p, k), m = static_cast<float*>(T.m)[k], v = static_cast<float*>(T.v)[k], r;
+            adam_update(a, gs, p, load_f<G>(T.g, k), m, v, r);
+            store_f<P>(T.p, k, p);
+            static_cast<float*>(T.m)[k] = m;
+            static_cast<float*>(T.v)[k] = v;
+            if (T.copy) store_copy(T.copy, a.ct, k, p);
+        }
+    }
 }
 
 // ---------------------------------------------------------------- gradient norm
@@ -195,14 +395,36 @@ __global__ void __launch_bounds__(kAdamThreads)
                 uint32_t* counter, float max_norm, float* out) {
     float s = 0.f;
     const uint32_t k0 = blockIdx.x * group, k1 = min(k0 + group, nchunks);
-    for (uint32_t k = k0; k < k1; ++k) {
+    uint32_t k = k0;
+    while (k < k1) {
         const AdamChunk c = chunks[k];
         const AdamTensor& T = tensors[c.tensor];
-        const uint64_t c0 = (uint64_t)c.index * kAdamChunk, c1 = min(c0 + kAdamChunk, T.n);
-        for (uint64_t i = c0 + threadIdx.x; i < c1; i += kAdamThreads) {
-            const float g = load_f<G>(T.g, i);
-            s = fmaf(g, g, s);
+        const int64_t i = (int64_t)((uint64_t)c.index * kAdamChunk + threadIdx.x * kAdamVec) - T.gphase;
+        const int64_t end = (int64_t)(((uint64_t)c.index + 4) * kAdamChunk) - T.gphase;
+        if (k + 4 <= k1 && c.index > 0 && end <= (int64_t)T.n) {     // four whole chunks of one tensor: loads together
+            float g[4][8];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) load8<G>(T.g, (uint64_t)i + u * kAdamChunk, g[u]);
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) s = fmaf(g[u][e], g[u][e], s);
+            k += 4;
+            continue;
         }
+        if (i >= 0 && (uint64_t)i + 8 <= T.n) {
+            float g[8];
+            load8<G>(T.g, (uint64_t)i, g);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s = fmaf(g[e], g[e], s);
+        } else {
+            for (int e = 0; e < 8; ++e)
+                if (i + e >= 0 && (uint64_t)(i + e) < T.n) {
+                    const float g = load_f<G>(T.g, (uint64_t)(i + e));
+                    s = fmaf(g, g, s);
+                }
+        }
+        ++k;
     }
     __shared__ double red[kAdamThreads / 32];
     __shared__ bool last;
@@ -303,7 +525,8 @@ sym_status_t sym_adamw_create(size_t ntensors, const size_t* counts, void* const
             const bool same = ph == phase_of(t.g, gs) && ph == phase_of(t.m, ss) && ph == phase_of(t.v, ss) &&
                               (!t.copy || ph == phase_of(t.copy, cs));
             t.phase = same && !(mx8 && ph) ? ph : -1;
-            const size_t span = n + (t.phase > 0 ? t.phase : 0);
+            t.gphase = phase_of(t.g, gs);
+            const size_t span = n + std::max(std::max(t.phase, 0), t.gphase);
             for (size_t k = 0; k < ceil_div(span, kAdamChunk); ++k) cks.push_back({(uint32_t)ts.size(), (uint32_t)k});
             if (cks.size() >= (1u << 31)) return SYM_ERR_UNSUPPORTED;
             ts.push_back(t);
@@ -393,6 +616,7 @@ sym_status_t sym_adamw_step(sym_adamw_t a, double lr, double beta1, double beta2
     k.step = (float)(lr / (1.0 - std::pow(beta1, (double)step)));
     k.seed = seed;
     k.ct = (int)a->ct;
+    k.nz.v = 0x8000000080000000ull;
     void* args[] = {&k};
     SYM_CUDA(cudaLaunchKernel(adam_kernel(a->pt, a->gt, a->mx8), dim3(a->nchunks), dim3(kAdamThreads), args, 0,
                               (cudaStream_t)stream));
