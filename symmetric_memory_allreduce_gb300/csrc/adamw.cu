@@ -48,6 +48,7 @@ struct AdamChunk {
 constexpr int kAdamThreads = 256;
 constexpr int kAdamVec = 8;                                     // elements per thread
 constexpr size_t kAdamChunk = (size_t)kAdamThreads * kAdamVec;  // elements per block
+constexpr uint32_t kStepGroupMax = 16;                           // chunks per block of the step, 8-bit states
 constexpr int kNormGroupMax = 32;                               // chunks per block of the norm
 
 }  // namespace symar
@@ -56,7 +57,7 @@ struct sym_adamw {
     int device;
     sym_dtype_t pt, gt, ct;
     bool mx8, has_copy;
-    uint32_t nchunks, norm_blocks, norm_group;
+    uint32_t nchunks, norm_blocks, norm_group, step_group;
     uint64_t total;
     void* mem;                        // one allocation: tensors, chunks, partials, counter
     symar::AdamTensor* tensors;
@@ -121,6 +122,7 @@ struct AdamArgs {
     float b1, b1c, b2, b2c;   // beta and 1 - beta
     float decay, rcorr, eps, step;
     uint32_t seed;
+    uint32_t nchunks, group;  // chunks in all, and per block
     int ct;                   // type of the copy
     F2 nz;                    // (-0, -0), see mul2
 };
@@ -137,7 +139,7 @@ __device__ __forceinline__ uint32_t e4m3_stochastic(float y, uint32_t h) {
     const uint32_t bits = __float_as_uint(y);
     const uint32_t eb = max(bits & 0x7F800000u, 121u << 23);
     const float u = __fadd_rn(__uint_as_float((h >> 9 & ~7u) | 0x3F800000u), -1.f);
-    const float z = __fadd_rn(__fmul_rn(y, __uint_as_float((257u << 23) - eb)), u);
+    const float z = fmaf(y, __uint_as_float((257u << 23) - eb), u);      // the product is exact
     const uint32_t code = (eb >> 20) + __float_as_uint(__fadd_rd(z, 0x1p23f)) - (968u + 0x4B000000u);
     return min(max(code, min(bits, 1u)), 0x7Fu);
 }
@@ -232,18 +234,25 @@ __device__ __forceinline__ void adam_chunk_scalar(const AdamArgs& a, const AdamT
 // Eight neighbouring elements by 16-byte (8-bit codes: 8-byte) accesses.  Every byte is used once:
 // streaming loads and stores, so that they do not displace what the next kernels read from L2.
 template <class T>
-__device__ __forceinline__ void load8(const void* base, uint64_t i, float (&f)[8]) {
-    const uint4* q = reinterpret_cast<const uint4*>(static_cast<const T*>(base) + i);
+__device__ __forceinline__ void unpack8(const uint4* q, float (&f)[8]) {
     if (sizeof(T) == 4) {
-        const uint4 a = __ldcs(q), b = __ldcs(q + 1);
+        const uint4 a = q[0], b = q[1];
         f[0] = __uint_as_float(a.x), f[1] = __uint_as_float(a.y), f[2] = __uint_as_float(a.z), f[3] = __uint_as_float(a.w);
         f[4] = __uint_as_float(b.x), f[5] = __uint_as_float(b.y), f[6] = __uint_as_float(b.z), f[7] = __uint_as_float(b.w);
     } else {
-        const uint4 a = __ldcs(q);
-        const T* h = reinterpret_cast<const T*>(&a);
+        const T* h = reinterpret_cast<const T*>(q);
 #pragma unroll
         for (int e = 0; e < 8; ++e) f[e] = to_f(h[e]);
     }
+}
+
+template <class T>
+__device__ __forceinline__ void load8(const void* base, uint64_t i, float (&f)[8]) {
+    const uint4* q = reinterpret_cast<const uint4*>(static_cast<const T*>(base) + i);
+    uint4 x[sizeof(T) / 2];
+#pragma unroll
+    for (int k = 0; k < (int)sizeof(T) / 2; ++k) x[k] = __ldcs(q + k);
+    unpack8<T>(x, f);
 }
 
 template <class T>
@@ -267,99 +276,136 @@ __device__ __forceinline__ void store_copy8(void* dst, int ct, uint64_t i, const
     else store8<float>(dst, i, p);
 }
 
-// One block per chunk of 2048 elements, 8 neighbouring ones per thread, counted from the vector
-// boundary at or before the tensor's start; a thread whose eight are not all inside goes one by one.
-template <class P, class G, bool MX8>
-__global__ void __launch_bounds__(kAdamThreads) k_adamw(AdamArgs a) {
-    const float gs = a.gscale ? __ldg(a.gscale) : 1.f;
-    const AdamChunk c = a.chunks[blockIdx.x];
-    const AdamTensor T = a.tensors[c.tensor];
-    if (!isfinite(gs)) return;                       // the step is skipped as a whole
-    const uint64_t c0 = (uint64_t)c.index * kAdamChunk;
-    if (T.phase < 0) return adam_chunk_scalar<P, G, MX8>(a, T, c0, gs);
-    const int64_t first = (int64_t)(c0 + threadIdx.x * kAdamVec) - T.phase;
-    const uint64_t i = (uint64_t)first;
-    if (MX8) {
-        // phase 0; four threads hold a scale block, so whole warps stay together
-        uint8_t* cm = static_cast<uint8_t*>(T.m);
-        uint8_t* cv = static_cast<uint8_t*>(T.v);
-        float p[8], g[8], m[8], r[8];
-        float am = 0.f, ar = 0.f;
-        const bool whole = i + 8 <= T.n;
-        if (whole) {
-            const uint2 xm = __ldcs(reinterpret_cast<const uint2*>(cm + i)), xv = __ldcs(reinterpret_cast<const uint2*>(cv + i));
-            const float sm = pow2i((int)T.ms[i >> 5] - 127), sv = pow2i((int)T.vs[i >> 5] - 127);
-            load8<P>(T.p, i, p);
-            load8<G>(T.g, i, g);
+__device__ __forceinline__ float min_nan(float x, float y) {
+    float r;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
+    return r;
+}
+
+// What eight neighbouring elements with 8-bit states are read as.
+template <class P, class G>
+struct RawMx8 {
+    uint4 p[sizeof(P) / 2], g[sizeof(G) / 2];
+    uint2 m, v;
+    uint32_t ms, vs;
+
+    __device__ __forceinline__ void load(const AdamTensor& T, uint64_t i) {
 #pragma unroll
-            for (int e = 0; e < 8; e += 2) {
-                e4m3_values2((e < 4 ? xm.x : xm.y) >> (e % 4 * 8), sm, a.nz, m + e);
-                e4m3_values2((e < 4 ? xv.x : xv.y) >> (e % 4 * 8), sv, a.nz, r + e);
-            }
-        } else {
+        for (int k = 0; k < (int)sizeof(P) / 2; ++k) p[k] = __ldcs(reinterpret_cast<const uint4*>(static_cast<const P*>(T.p) + i) + k);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const bool in = i + e < T.n;
-                p[e] = in ? load_f<P>(T.p, i + e) : 0.f;
-                g[e] = in ? load_f<G>(T.g, i + e) : 0.f;
-                m[e] = in ? __fmul_rn(e4m3_value(cm[i + e]), pow2i((int)T.ms[(i + e) >> 5] - 127)) : 0.f;
-                r[e] = in ? __fmul_rn(e4m3_value(cv[i + e]), pow2i((int)T.vs[(i + e) >> 5] - 127)) : 0.f;
-            }
-        }
+        for (int k = 0; k < (int)sizeof(G) / 2; ++k) g[k] = __ldcs(reinterpret_cast<const uint4*>(static_cast<const G*>(T.g) + i) + k);
+        m = __ldcs(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(T.m) + i));
+        v = __ldcs(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(T.v) + i));
+        ms = T.ms[i >> 5];
+        vs = T.vs[i >> 5];
+    }
+};
+
+// Elements i .. i+7 of a tensor with 8-bit states (phase 0), read before as `x` where all are inside.
+// Four threads hold a scale block, so whole warps stay together.
+template <class P, class G>
+__device__ __forceinline__ void adam_eight_mx8(const AdamArgs& a, const AdamTensor& T, uint64_t i, bool whole,
+                                               const RawMx8<P, G>& x, float gs) {
+    uint8_t* cm = static_cast<uint8_t*>(T.m);
+    uint8_t* cv = static_cast<uint8_t*>(T.v);
+    float p[8], g[8], m[8], r[8];
+    float am = 0.f, ar = 0.f;
+    if (whole) {
+        const float sm = pow2i((int)x.ms - 127), sv = pow2i((int)x.vs - 127);
+        unpack8<P>(x.p, p);
+        unpack8<G>(x.g, g);
 #pragma unroll
         for (int e = 0; e < 8; e += 2) {
-            float v[2];
-            split(mul2(f2(r[e], r[e + 1]), f2(r[e], r[e + 1]), a.nz), v[0], v[1]);
-            adam_update2(a, gs, p + e, g + e, m + e, v, r + e);
+            e4m3_values2((e < 4 ? x.m.x : x.m.y) >> (e % 4 * 8), sm, a.nz, m + e);
+            e4m3_values2((e < 4 ? x.v.x : x.v.y) >> (e % 4 * 8), sv, a.nz, r + e);
         }
+    } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            if (!whole && i + e >= T.n) m[e] = r[e] = 0.f;
-            am = fmaxf(am, fabsf(m[e]));
-            ar = fmaxf(ar, r[e]);
+            const bool in = i + e < T.n;
+            p[e] = in ? load_f<P>(T.p, i + e) : 0.f;
+            g[e] = in ? load_f<G>(T.g, i + e) : 0.f;
+            m[e] = in ? __fmul_rn(e4m3_value(cm[i + e]), pow2i((int)T.ms[(i + e) >> 5] - 127)) : 0.f;
+            r[e] = in ? __fmul_rn(e4m3_value(cv[i + e]), pow2i((int)T.vs[(i + e) >> 5] - 127)) : 0.f;
         }
+    }
 #pragma unroll
-        for (int o = 1; o < 4; o <<= 1) {
-            am = fmaxf(am, __shfl_xor_sync(~0u, am, o));
-            ar = fmaxf(ar, __shfl_xor_sync(~0u, ar, o));
-        }
-        const int em = block_exponent(am), er = block_exponent(ar);
-        const float fm = pow2i(-em), fr = pow2i(-er);
-        uint32_t ym[2] = {0, 0}, yv[2] = {0, 0};
-        const uint32_t h0 = ((uint32_t)i + T.base) * 0x9E3779B1u + a.seed;
+    for (int e = 0; e < 8; e += 2) {
+        float v[2];
+        split(mul2(f2(r[e], r[e + 1]), f2(r[e], r[e + 1]), a.nz), v[0], v[1]);
+        adam_update2(a, gs, p + e, g + e, m + e, v, r + e);
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        if (!whole && i + e >= T.n) m[e] = r[e] = 0.f;
+        am = fmaxf(am, fabsf(m[e]));
+        ar = fmaxf(ar, r[e]);
+    }
+#pragma unroll
+    for (int o = 1; o < 4; o <<= 1) {
+        am = fmaxf(am, __shfl_xor_sync(~0u, am, o));
+        ar = fmaxf(ar, __shfl_xor_sync(~0u, ar, o));
+    }
+    const int em = block_exponent(am), er = block_exponent(ar);
+    const float fm = pow2i(-em), fr = pow2i(-er);
+    uint32_t ym[2] = {0, 0}, yv[2] = {0, 0};
+    const uint32_t h0 = ((uint32_t)i + T.base) * 0x9E3779B1u + a.seed;
+    // Roots that scale to normal e4m3 numbers need no floating point: 20 random bits added to the 20
+    // that go, and the exponents' difference taken off.  A NaN fails the comparison.
+    const float lo = fmaxf(__fmul_rn(pow2i(er), 0x1p-6f), 0x1p-126f);
+    float least = min_nan(r[0], r[1]);
+#pragma unroll
+    for (int e = 2; e < 8; ++e) least = min_nan(least, r[e]);
+    if (least >= lo && ar <= 3.4e38f) {
+        const uint32_t k = (uint32_t)(er + 120) << 23;
+        uint32_t t[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) t[e] = (__float_as_uint(r[e]) - k + (mix32(h0 + e * 0x9E3779B1u) >> 12)) << 4;
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+            yv[q] = __byte_perm(__byte_perm(t[4 * q], t[4 * q + 1], 0x0073), __byte_perm(t[4 * q + 2], t[4 * q + 3], 0x0073), 0x5410);
+    } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e)
             yv[e / 4] |= e4m3_stochastic(__fmul_rn(r[e], fr), mix32(h0 + e * 0x9E3779B1u)) << (e % 4 * 8);
-        if (am <= 3.4e38f) {
+    }
+    if (am <= 3.4e38f) {
 #pragma unroll
-            for (int e = 0; e < 8; e += 2)
-                ym[e / 4] |= (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(__fmul_rn(m[e], fm), __fmul_rn(m[e + 1], fm)),
-                                                                __NV_SATFINITE, __NV_E4M3)
-                             << (e % 4 * 8);
-        } else {
+        for (int e = 0; e < 8; e += 2)
+            ym[e / 4] |= (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(__fmul_rn(m[e], fm), __fmul_rn(m[e + 1], fm)),
+                                                            __NV_SATFINITE, __NV_E4M3)
+                         << (e % 4 * 8);
+    } else {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) ym[e / 4] |= (uint32_t)e4m3_nearest(__fmul_rn(m[e], fm)) << (e % 4 * 8);
-        }
-        if (whole) {
-            store8<P>(T.p, i, p);
-            if (T.copy) store_copy8(T.copy, a.ct, i, p);
-            __stcs(reinterpret_cast<uint2*>(cm + i), make_uint2(ym[0], ym[1]));
-            __stcs(reinterpret_cast<uint2*>(cv + i), make_uint2(yv[0], yv[1]));
-        } else {
+        for (int e = 0; e < 8; ++e) ym[e / 4] |= (uint32_t)e4m3_nearest(__fmul_rn(m[e], fm)) << (e % 4 * 8);
+    }
+    if (whole) {
+        store8<P>(T.p, i, p);
+        if (T.copy) store_copy8(T.copy, a.ct, i, p);
+        __stcs(reinterpret_cast<uint2*>(cm + i), make_uint2(ym[0], ym[1]));
+        __stcs(reinterpret_cast<uint2*>(cv + i), make_uint2(yv[0], yv[1]));
+    } else {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                if (i + e >= T.n) break;
-                store_f<P>(T.p, i + e, p[e]);
-                if (T.copy) store_copy(T.copy, a.ct, i + e, p[e]);
-                cm[i + e] = (uint8_t)(ym[e / 4] >> (e % 4 * 8));
-                cv[i + e] = (uint8_t)(yv[e / 4] >> (e % 4 * 8));
-            }
+        for (int e = 0; e < 8; ++e) {
+            if (i + e >= T.n) break;
+            store_f<P>(T.p, i + e, p[e]);
+            if (T.copy) store_copy(T.copy, a.ct, i + e, p[e]);
+            cm[i + e] = (uint8_t)(ym[e / 4] >> (e % 4 * 8));
+            cv[i + e] = (uint8_t)(yv[e / 4] >> (e % 4 * 8));
         }
-        if ((threadIdx.x & 3) == 0 && i < T.n) {
-            T.ms[i >> 5] = (uint8_t)(em + 127);
-            T.vs[i >> 5] = (uint8_t)(er + 127);
-        }
-    } else if (first >= 0 && i + 8 <= T.n) {
+    }
+    if ((threadIdx.x & 3) == 0 && i < T.n) {
+        T.ms[i >> 5] = (uint8_t)(em + 127);
+        T.vs[i >> 5] = (uint8_t)(er + 127);
+    }
+}
+
+// Eight neighbouring elements with 32-bit states, from element `first`, not all of them inside at the
+// tensor's ends.
+template <class P, class G>
+__device__ __forceinline__ void adam_eight_f32(const AdamArgs& a, const AdamTensor& T, int64_t first, float gs) {
+    const uint64_t i = (uint64_t)first;
+    if (first >= 0 && i + 8 <= T.n) {
         float p[8], g[8], m[8], v[8], r[2];
         load8<P>(T.p, i, p);
         load8<G>(T.g, i, g);
@@ -382,6 +428,45 @@ __global__ void __launch_bounds__(kAdamThreads) k_adamw(AdamArgs a) {
             static_cast<float*>(T.v)[k] = v;
             if (T.copy) store_copy(T.copy, a.ct, k, p);
         }
+    }
+}
+
+// A block takes `group` chunks of 2048 elements, 8 neighbouring ones per thread, counted from the vector
+// boundary at or before the tensor's start.
+template <class P, class G, bool MX8>
+__global__ void __launch_bounds__(kAdamThreads, MX8 ? 3 : 4) k_adamw(AdamArgs a) {
+    const float gs = a.gscale ? __ldg(a.gscale) : 1.f;
+    if (!isfinite(gs)) return;                       // the step is skipped as a whole
+    const uint32_t k1 = min((blockIdx.x + 1) * a.group, a.nchunks);
+    uint32_t k = blockIdx.x * a.group;
+    while (k < k1) {
+        const uint32_t ti = a.chunks[k].tensor;
+        const AdamTensor T = a.tensors[ti];
+        uint64_t c0 = (uint64_t)a.chunks[k].index * kAdamChunk;
+        uint32_t run = 1;                            // chunks of this tensor
+        while (k + run < k1 && a.chunks[k + run].tensor == ti) ++run;
+        if (T.phase < 0 || !MX8) {
+#pragma unroll 1
+            for (uint32_t u = 0; u < run; ++u, c0 += kAdamChunk) {
+                if (T.phase < 0) adam_chunk_scalar<P, G, MX8>(a, T, c0, gs);
+                else adam_eight_f32<P, G>(a, T, (int64_t)(c0 + threadIdx.x * kAdamVec) - T.phase, gs);
+            }
+        } else {
+            // the next chunk's reads are under way while this one is computed
+            uint64_t i = c0 + threadIdx.x * kAdamVec;
+            RawMx8<P, G> x, next;
+            bool whole = i + 8 <= T.n;
+            if (whole) x.load(T, i);
+#pragma unroll 1
+            for (uint32_t u = 0; u < run; ++u, i += kAdamChunk) {
+                const bool more = u + 1 < run && i + kAdamChunk + 8 <= T.n;
+                if (more) next.load(T, i + kAdamChunk);
+                adam_eight_mx8<P, G>(a, T, i, whole, x, gs);
+                x = next;
+                whole = more;
+            }
+        }
+        k += run;
     }
 }
 
@@ -549,6 +634,11 @@ sym_status_t sym_adamw_create(size_t ntensors, const size_t* counts, void* const
         // the norm's blocks: a few per SM at least, up to 32 chunks each
         a->norm_group = (uint32_t)std::min<size_t>(std::max<size_t>(cks.size() / (size_t)(ctx->num_sms * 16), 1),
                                                    kNormGroupMax);
+        // 8-bit states: several chunks per block, so that one's reads run under another's arithmetic,
+        // as long as there are 8 blocks for each of the 3 a SM holds
+        a->step_group = mx8 ? (uint32_t)std::min<size_t>(std::max<size_t>(cks.size() / (ctx->num_sms * 24), 1),
+                                                         kStepGroupMax)
+                            : 1;
         a->norm_blocks = (uint32_t)ceil_div(cks.size(), (size_t)a->norm_group);
         const size_t tb = ceil_div(ts.size() * sizeof(AdamTensor), (size_t)256) * 256;
         const size_t cb = ceil_div(cks.size() * sizeof(AdamChunk), (size_t)256) * 256;
@@ -615,10 +705,13 @@ sym_status_t sym_adamw_step(sym_adamw_t a, double lr, double beta1, double beta2
     k.eps = (float)eps;
     k.step = (float)(lr / (1.0 - std::pow(beta1, (double)step)));
     k.seed = seed;
+    k.nchunks = a->nchunks;
+    k.group = a->step_group;
     k.ct = (int)a->ct;
     k.nz.v = 0x8000000080000000ull;
     void* args[] = {&k};
-    SYM_CUDA(cudaLaunchKernel(adam_kernel(a->pt, a->gt, a->mx8), dim3(a->nchunks), dim3(kAdamThreads), args, 0,
+    SYM_CUDA(cudaLaunchKernel(adam_kernel(a->pt, a->gt, a->mx8), dim3((a->nchunks - 1) / a->step_group + 1),
+                              dim3(kAdamThreads), args, 0,
                               (cudaStream_t)stream));
     count_launch();
     return SYM_OK;

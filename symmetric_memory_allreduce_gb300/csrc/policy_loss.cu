@@ -12,6 +12,7 @@
 // its outputs are 0 whatever stands there.
 #include <cmath>
 
+#include "tensor.cuh"
 #include "training.cuh"
 
 namespace symar {
@@ -62,12 +63,12 @@ __device__ __forceinline__ RowTerms row_terms(const PolicyArgs& a, size_t t, flo
 }
 
 // The row's weight, 0 (with the status word set) where its target is no column.
-__device__ __forceinline__ float row_weight(const PolicyArgs& a, size_t t) {
+__device__ __forceinline__ float row_weight(const PolicyArgs& a, size_t t, bool report) {
     const float w = a.weights ? a.weights[t] : 1.f;
     if (w == 0.f) return 0.f;
     const int64_t y = a.targets[t];
     if (y >= 0 && (uint64_t)y < a.V) return w;
-    if (threadIdx.x == 0 && (atomicOr(a.status, kStatusBadArg) & kStatusBadArg) == 0) {
+    if (report && threadIdx.x == 0 && (atomicOr(a.status, kStatusBadArg) & kStatusBadArg) == 0) {
         a.status[1] = kSitePolicyTarget;
         a.status[2] = (uint32_t)t;
         a.status[3] = (uint32_t)y;
@@ -75,12 +76,276 @@ __device__ __forceinline__ float row_weight(const PolicyArgs& a, size_t t) {
     return 0.f;
 }
 
+// One element of a row, as 16-byte vectors of E elements counted from the 16-byte boundary at or
+// before the row's start: vector v holds elements v*E - phase and on.
+template <class X>
+struct Row {
+    static constexpr int E = 16 / sizeof(X);
+    X* p;
+    int phase;
+    __device__ __forceinline__ Row(const void* base, size_t at) {
+        p = const_cast<X*>(static_cast<const X*>(base)) + at;
+        phase = (int)((uintptr_t)p / sizeof(X) % E);
+    }
+};
+
+template <class X>
+__device__ __forceinline__ uint32_t minus_inf_bits();
+template <>
+__device__ __forceinline__ uint32_t minus_inf_bits<float>() { return 0xFF800000u; }
+template <>
+__device__ __forceinline__ uint32_t minus_inf_bits<__nv_bfloat16>() { return 0xFF80FF80u; }
+template <>
+__device__ __forceinline__ uint32_t minus_inf_bits<__half>() { return 0xFC00FC00u; }
+
+template <class X>
+__device__ __forceinline__ void unpack(const uint4& v, float (&f)[Row<X>::E]) {
+    const X* h = reinterpret_cast<const X*>(&v);
+#pragma unroll
+    for (int e = 0; e < Row<X>::E; ++e) f[e] = to_f(h[e]);
+}
+
+// Vector v of a row; what lies outside the row's V elements reads as -infinity (weight 0).
+template <class X>
+__device__ __forceinline__ uint4 load_vector(const Row<X>& r, int64_t v, int64_t V) {
+    constexpr int E = Row<X>::E;
+    const int64_t j = v * E - r.phase;
+    if (j >= 0 && j + E <= V) return __ldcs(reinterpret_cast<const uint4*>(r.p + j));
+    const uint32_t inf = minus_inf_bits<X>();
+    uint4 x = make_uint4(inf, inf, inf, inf);
+    X* h = reinterpret_cast<X*>(&x);
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+        if (j + e >= 0 && j + e < V) h[e] = r.p[j + e];
+    return x;
+}
+
+// Writes the elements of vector v (counted in a row with `phase`) that are inside.
+template <class X>
+__device__ __forceinline__ void store_vector(const Row<X>& r, int phase, int64_t v, int64_t V, const uint4& x) {
+    constexpr int E = Row<X>::E;
+    const int64_t j = v * E - phase;
+    if (phase == r.phase && j >= 0 && j + E <= V) {
+        __stcs(reinterpret_cast<uint4*>(r.p + j), x);
+        return;
+    }
+    const X* h = reinterpret_cast<const X*>(&x);
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+        if (j + e >= 0 && j + e < V) r.p[j + e] = h[e];
+}
+
+__device__ __forceinline__ float exp2_approx(float x) {      // 2 ulp; exp2(-inf) = 0
+    float y;
+    asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Running maximum m and sum s of exp2(c x - c m) over a vector's elements.
+template <class X>
+__device__ __forceinline__ void add_vector(const uint4& v, float c, float& m, float& s) {
+    constexpr int E = Row<X>::E;
+    float x[E];
+    unpack<X>(v, x);
+    float M = m;
+#pragma unroll
+    for (int e = 0; e < E; ++e) M = fmaxf(M, x[e]);
+    const float b = M == -INFINITY ? 0.f : M * c;            // all -inf so far: every term is 0
+    s *= m == M ? 1.f : exp2_approx(fmaf(m, c, -b));
+#pragma unroll
+    for (int e = 0; e < E; ++e) s += exp2_approx(fmaf(x[e], c, -b));
+    m = M;
+}
+
+// Joins two (maximum, sum) pairs.
+__device__ __forceinline__ void join(float c, float& m, float& s, float m2, float s2) {
+    const float M = fmaxf(m, m2), b = M == -INFINITY ? 0.f : M * c;
+    s = s * exp2_approx(fmaf(m, c, -b)) + s2 * exp2_approx(fmaf(m2, c, -b));
+    m = M;
+}
+
+// The gradient's common factors of a row: dlogits_j = -coef exp2(c x_j - lse2) (+ coef at the target).
+struct RowGrad {
+    float shift;               // log2|coef| - lse2
+    uint32_t flip;             // sign bits of -coef, for one 32-bit word of X
+    float coef, lse2;
+};
+
+template <class X>
+__device__ __forceinline__ RowGrad row_grad(float coef, float lse) {
+    RowGrad g;
+    g.coef = coef;
+    g.lse2 = lse * 1.44269504f;
+    g.shift = log2f(fabsf(coef)) - g.lse2;
+    g.flip = coef > 0.f ? (sizeof(X) == 4 ? 0x80000000u : 0x80008000u) : 0u;
+    return g;
+}
+
+// Its magnitudes are 2^(c x + shift): one product, one exponential, one rounding an element; the sign
+// is set on the rounded word.
+template <class X>
+__device__ __forceinline__ uint4 grad_vector(const uint4& v, float c, const RowGrad& g) {
+    constexpr int E = Row<X>::E;
+    float x[E];
+    unpack<X>(v, x);
+    uint4 o;
+    X* h = reinterpret_cast<X*>(&o);
+#pragma unroll
+    for (int e = 0; e < E; ++e) h[e] = from_f<X>(exp2_approx(fmaf(x[e], c, g.shift)));
+    o.x ^= g.flip, o.y ^= g.flip, o.z ^= g.flip, o.w ^= g.flip;
+    return o;
+}
+
+// The target's element, by the thread that wrote its vector, after it.
+template <class X>
+__device__ __forceinline__ void fix_target(const Row<X>& d, int phase, int64_t v, int64_t y, float c, float xy,
+                                           const RowGrad& g) {
+    const int64_t j = v * Row<X>::E - phase;
+    if (y >= j && y < j + Row<X>::E) d.p[y] = from_f<X>(g.coef - g.coef * exp2_approx(fmaf(xy, c, -g.lse2)));
+}
+
+// A cluster of CTAs per row (1, 2, 4 or 8), each with a run of its vectors, VPT a thread at a time,
+// neighbouring threads on neighbouring vectors.  KEEP: the run fits the threads' registers, so the
+// logits are read once and the gradient comes from registers; else they are read again for it.
+template <class X, int THREADS, int VPT, bool KEEP>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) k_policy_loss(PolicyArgs a, int64_t run) {
+    __shared__ float s_m[THREADS / 32], s_s[THREADS / 32], s_cm[8], s_cs[8];
+    __shared__ RowGrad s_g;
+    uint32_t rank = 0, C = 1;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+    asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(C));
+    const size_t t = blockIdx.x / C;
+    const int64_t V = (int64_t)a.V;
+    const Row<X> x(a.logits, t * a.ld), d(a.dlogits, a.dlogits ? t * a.ldd : 0);
+    const int64_t vectors = (V + x.phase + Row<X>::E - 1) / Row<X>::E;
+    const int64_t v0 = (int64_t)rank * run + threadIdx.x, v1 = min((int64_t)(rank + 1) * run, vectors);
+    uint4 r[VPT];
+    const float w = row_weight(a, t, rank == 0);
+    if (w == 0.f) {                                          // the same in every CTA of the cluster
+        if (rank == 0 && threadIdx.x == 0) a.logp[t] = a.lse[t] = 0.f;
+        if (a.dlogits)
+            for (int64_t v = v0; v < v1; v += THREADS) store_vector<X>(d, x.phase, v, V, make_uint4(0, 0, 0, 0));
+        return;
+    }
+    if (C > 1) cluster_arrive();                             // waited for before the first remote store
+    const float c = a.inv_t * 1.44269504f;
+    float m = -INFINITY, s = 0.f;
+    for (int64_t v = v0; v < v1; v += (int64_t)THREADS * VPT) {
+        const uint32_t inf = minus_inf_bits<X>();
+#pragma unroll
+        for (int k = 0; k < VPT; ++k)
+            r[k] = v + k * THREADS < v1 ? load_vector<X>(x, v + k * THREADS, V) : make_uint4(inf, inf, inf, inf);
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) add_vector<X>(r[k], c, m, s);
+        if (KEEP) break;
+    }
+    const int64_t y = a.targets[t];
+    const float xy = to_f(x.p[y]);                           // before a gradient in place can replace it
+    const float wm = warp_max(m);
+    s = warp_sum(s * exp2_approx(fmaf(m, c, wm == -INFINITY ? 0.f : -wm * c)));
+    if (threadIdx.x % 32 == 0) {
+        s_m[threadIdx.x / 32] = wm;
+        s_s[threadIdx.x / 32] = s;
+    }
+    __syncthreads();
+    if (C > 1) cluster_wait();
+    if (threadIdx.x < 32) {
+        constexpr int W = THREADS / 32;
+        m = threadIdx.x < W ? s_m[threadIdx.x] : -INFINITY;
+        s = threadIdx.x < W ? s_s[threadIdx.x] : 0.f;
+#pragma unroll
+        for (int o = 1; o < W; o <<= 1) join(c, m, s, __shfl_xor_sync(~0u, m, o), __shfl_xor_sync(~0u, s, o));
+        if (C > 1 && threadIdx.x < C) {                      // to every CTA of the cluster
+            st_cluster_f32(map_rank(smem_u32(&s_cm[rank]), threadIdx.x), m);
+            st_cluster_f32(map_rank(smem_u32(&s_cs[rank]), threadIdx.x), s);
+        }
+    }
+    if (C > 1) {
+        __syncwarp();
+        cluster_sync();
+    }
+    if (threadIdx.x == 0) {
+        if (C > 1) {
+            m = s_cm[0], s = s_cs[0];
+            for (uint32_t q = 1; q < C; ++q) join(c, m, s, s_cm[q], s_cs[q]);
+        }
+        const float lse = m * a.inv_t + logf(s), logp = xy * a.inv_t - lse;
+        if (rank == 0) {
+            a.logp[t] = logp;
+            a.lse[t] = lse;
+        }
+        if (a.dlogits) {
+            const float go = a.grad_out ? *a.grad_out : 1.f;
+            s_g = row_grad<X>(go * w * row_terms(a, t, logp).slope * a.inv_t, lse);
+        }
+    }
+    if (!a.dlogits) return;
+    __syncthreads();
+    const RowGrad g = s_g;
+    for (int64_t v = v0; v < v1; v += (int64_t)THREADS * VPT) {
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) {
+            const int64_t u = v + k * THREADS;
+            if (u >= v1) break;
+            if (!KEEP) r[k] = load_vector<X>(x, u, V);
+            store_vector<X>(d, x.phase, u, V, grad_vector<X>(r[k], c, g));
+            fix_target<X>(d, x.phase, u, y, c, xy, g);
+        }
+        if (KEEP) break;
+    }
+}
+
+// The gradient alone: a block takes kBackThreads * kBackVectors vectors of a row.
+constexpr int kBackThreads = 256, kBackVectors = 4;
+
+template <class X>
+__global__ void __launch_bounds__(kBackThreads) k_policy_backward(PolicyArgs a, uint32_t blocks_per_row) {
+    __shared__ RowGrad s_g;
+    const size_t t = blockIdx.x / blocks_per_row;
+    const int64_t V = (int64_t)a.V;
+    const Row<X> x(a.logits, t * a.ld), d(a.dlogits, t * a.ldd);
+    const int64_t v0 = (int64_t)(blockIdx.x % blocks_per_row) * (kBackThreads * kBackVectors) + threadIdx.x;
+    const int64_t vectors = (V + x.phase + Row<X>::E - 1) / Row<X>::E;
+    const float w = row_weight(a, t, blockIdx.x % blocks_per_row == 0);
+    if (w == 0.f) {
+#pragma unroll
+        for (int k = 0; k < kBackVectors; ++k)
+            if (v0 + k * kBackThreads < vectors)
+                store_vector<X>(d, x.phase, v0 + k * kBackThreads, V, make_uint4(0, 0, 0, 0));
+        return;
+    }
+    uint4 r[kBackVectors];
+#pragma unroll
+    for (int k = 0; k < kBackVectors; ++k)
+        if (v0 + k * kBackThreads < vectors) r[k] = load_vector<X>(x, v0 + k * kBackThreads, V);
+    const int64_t y = a.targets[t];
+    const float c = a.inv_t * 1.44269504f;
+    if (threadIdx.x == 0) {
+        const float go = a.grad_out ? *a.grad_out : 1.f;
+        s_g = row_grad<X>(go * w * row_terms(a, t, a.logp[t]).slope * a.inv_t, a.lse[t]);
+    }
+    __syncthreads();
+    const RowGrad g = s_g;
+#pragma unroll
+    for (int k = 0; k < kBackVectors; ++k) {
+        const int64_t v = v0 + k * kBackThreads, j = v * Row<X>::E - x.phase;
+        if (v >= vectors) break;
+        const bool target = y >= j && y < j + Row<X>::E;
+        const float xy = target ? to_f(x.p[y]) : 0.f;        // this thread's own vector: not yet replaced
+        store_vector<X>(d, x.phase, v, V, grad_vector<X>(r[k], c, g));
+        if (target) fix_target<X>(d, x.phase, v, y, c, xy, g);
+    }
+}
+
 // stats = {loss, policy part, kl, weight of clipped rows}, summed in a fixed order by one
 // block of a launch of its own: a counter that finds the last block of the first launch would
 // have to live somewhere, and two calls in flight (or a replayed graph) would share it.
+constexpr int kStatsThreads = 512;
+
 template <int THREADS>
 __global__ void __launch_bounds__(THREADS) k_policy_stats(PolicyArgs a) {
     __shared__ double red[THREADS / 32];
+    asm volatile("griddepcontrol.wait;" ::: "memory");       // launched while the rows' kernel still runs
     double s[4] = {0., 0., 0., 0.};
     for (size_t t = threadIdx.x; t < a.T; t += THREADS) {
         float w = a.weights ? a.weights[t] : 1.f;
@@ -98,85 +363,56 @@ __global__ void __launch_bounds__(THREADS) k_policy_stats(PolicyArgs a) {
     }
 }
 
-constexpr int kLossThreads = 512;
-constexpr int kStatsThreads = 512;
+// CTAs per row, threads and vectors per thread: the smallest block that holds the row in registers, the
+// row shared out further while there are fewer CTAs than SMs.
+struct LossShape {
+    int threads, vpt;
+    uint32_t cluster;
+    bool keep;
+};
 
-template <class X>
-__device__ __forceinline__ void write_gradient(const PolicyArgs& a, size_t t, float c, float lse) {
-    const X* x = static_cast<const X*>(a.logits) + t * a.ld;
-    X* g = static_cast<X*>(a.dlogits) + t * a.ldd;
-    const size_t y = (size_t)a.targets[t];
-    for (size_t j = threadIdx.x; j < a.V; j += kLossThreads) {
-        float v = -c * expf(to_f(x[j]) * a.inv_t - lse);
-        if (j == y) v += c;
-        g[j] = from_f<X>(v);
-    }
+static LossShape loss_shape(size_t T, size_t vectors, int num_sms) {
+    LossShape s{128, 2, 1, true};
+    while (s.vpt < 8 && (size_t)s.threads * s.vpt < vectors) s.vpt *= 2;
+    if ((size_t)s.threads * s.vpt < vectors) s = {512, 4, 1, true};
+    if ((size_t)s.threads * s.vpt < vectors) s.vpt = 8;
+    while (s.cluster < 8 && (size_t)s.threads * s.vpt * s.cluster < vectors) s.cluster *= 2;
+    while (s.cluster < 8 && s.vpt > 2 && T * s.cluster < (size_t)num_sms) s.cluster *= 2, s.vpt /= 2;
+    s.keep = (size_t)s.threads * s.vpt * s.cluster >= vectors;
+    return s;
 }
 
 template <class X>
-__device__ __forceinline__ void write_zeros(const PolicyArgs& a, size_t t) {
-    X* g = static_cast<X*>(a.dlogits) + t * a.ldd;
-    for (size_t j = threadIdx.x; j < a.V; j += kLossThreads) g[j] = from_f<X>(0.f);
-}
-
-template <class X>
-__global__ void __launch_bounds__(kLossThreads) k_policy_loss(PolicyArgs a) {
-    __shared__ float s_m[kLossThreads / 32], s_s[kLossThreads / 32];
-    const size_t t = blockIdx.x;
-    const float w = row_weight(a, t);
-    if (w == 0.f) {
-        if (threadIdx.x == 0) a.logp[t] = a.lse[t] = 0.f;
-        if (a.dlogits) write_zeros<X>(a, t);
-    } else {
-        const X* x = static_cast<const X*>(a.logits) + t * a.ld;
-        float m = -INFINITY, s = 0.f;
-        for (size_t j = threadIdx.x; j < a.V; j += kLossThreads) {
-            const float z = to_f(x[j]) * a.inv_t;
-            const float M = fmaxf(m, z);
-            if (M != -INFINITY) s = s * expf(m - M) + expf(z - M);
-            else if (z != z) s = z;
-            m = M;
-        }
-        const float wm = warp_max(m);
-        s = warp_sum(wm == -INFINITY ? s : s * expf(m - wm));
-        if ((threadIdx.x & 31) == 0) {
-            s_m[threadIdx.x >> 5] = wm;
-            s_s[threadIdx.x >> 5] = s;
-        }
-        __syncthreads();
-        m = -INFINITY;
-        for (int i = 0; i < kLossThreads / 32; ++i) m = fmaxf(m, s_m[i]);
-        s = 0.f;
-        for (int i = 0; i < kLossThreads / 32; ++i) s += m == -INFINITY ? s_s[i] : s_s[i] * expf(s_m[i] - m);
-        const float lse = m + logf(s);
-        const float logp = to_f(x[(size_t)a.targets[t]]) * a.inv_t - lse;
-        if (threadIdx.x == 0) {
-            a.logp[t] = logp;
-            a.lse[t] = lse;
-        }
-        if (a.dlogits) {
-            const float go = a.grad_out ? *a.grad_out : 1.f;
-            __syncthreads();                       // the target's logit is read before in-place gradients replace it
-            write_gradient<X>(a, t, go * w * row_terms(a, t, logp).slope * a.inv_t, lse);
-        }
-    }
-}
-
-template <class X>
-__global__ void __launch_bounds__(kLossThreads) k_policy_backward(PolicyArgs a) {
-    const size_t t = blockIdx.x;
-    const float w = row_weight(a, t);
-    if (w == 0.f) {
-        write_zeros<X>(a, t);
-        return;
-    }
-    const float go = a.grad_out ? *a.grad_out : 1.f;
-    write_gradient<X>(a, t, go * w * row_terms(a, t, a.logp[t]).slope * a.inv_t, a.lse[t]);
+static const void* loss_kernel(const LossShape& s) {
+    if (!s.keep) return (const void*)k_policy_loss<X, 512, 8, false>;
+    if (s.threads == 128)
+        return s.vpt == 2   ? (const void*)k_policy_loss<X, 128, 2, true>
+               : s.vpt == 4 ? (const void*)k_policy_loss<X, 128, 4, true>
+                            : (const void*)k_policy_loss<X, 128, 8, true>;
+    return s.vpt == 2   ? (const void*)k_policy_loss<X, 512, 2, true>
+           : s.vpt == 4 ? (const void*)k_policy_loss<X, 512, 4, true>
+                        : (const void*)k_policy_loss<X, 512, 8, true>;
 }
 
 }  // namespace symar
 
 using namespace symar;
+
+// A launch with one attribute: a cluster size, or leave to start before the kernel before it has ended.
+static cudaError_t launch_with(const void* kernel, unsigned grid, int threads, void** args, cudaStream_t st,
+                               cudaLaunchAttributeID id, uint32_t value) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.stream = st;
+    cudaLaunchAttribute attr{};
+    attr.id = id;
+    if (id == cudaLaunchAttributeClusterDimension) attr.val.clusterDim.x = value, attr.val.clusterDim.y = 1, attr.val.clusterDim.z = 1;
+    else attr.val.programmaticStreamSerializationAllowed = (int)value;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelExC(&cfg, kernel, args);
+}
 
 static sym_status_t check_policy(const PolicyArgs& a, sym_dtype_t dtype, double clip_low, double clip_high,
                                  double kl_coef, double temperature) {
@@ -225,12 +461,23 @@ sym_status_t sym_policy_loss(const void* logits, size_t ld, size_t rows, size_t 
     if (!ctx) return SYM_ERR_CUDA;
     cudaStream_t st = (cudaStream_t)stream;
     a.status = ctx->status;
-    if (rows) switch (dtype) {
-        case SYM_F32: k_policy_loss<float><<<(unsigned)rows, kLossThreads, 0, st>>>(a); break;
-        case SYM_BF16: k_policy_loss<__nv_bfloat16><<<(unsigned)rows, kLossThreads, 0, st>>>(a); break;
-        case SYM_F16: k_policy_loss<__half><<<(unsigned)rows, kLossThreads, 0, st>>>(a); break;
+    if (rows) {
+        const size_t per = 16 / dtype_size(dtype), vectors = ceil_div(vocab + per - 1, per);
+        const LossShape sh = loss_shape(rows, vectors, ctx->num_sms);
+        if (rows * sh.cluster >= (1ull << 31)) return SYM_ERR_UNSUPPORTED;
+        int64_t run = (int64_t)ceil_div(vectors, (size_t)sh.cluster);
+        const void* k = dtype == SYM_F32    ? loss_kernel<float>(sh)
+                        : dtype == SYM_BF16 ? loss_kernel<__nv_bfloat16>(sh)
+                                            : loss_kernel<__half>(sh);
+        void* args[] = {&a, &run};
+        SYM_CUDA(launch_with(k, (unsigned)(rows * sh.cluster), sh.threads, args, st,
+                             cudaLaunchAttributeClusterDimension, sh.cluster));
     }
-    k_policy_stats<kStatsThreads><<<1, kStatsThreads, 0, st>>>(a);
+    {
+        void* args[] = {&a};
+        SYM_CUDA(launch_with((const void*)k_policy_stats<kStatsThreads>, 1, kStatsThreads, args, st,
+                             cudaLaunchAttributeProgrammaticStreamSerialization, 1));
+    }
     count_launch(rows ? 2 : 1);
     SYM_CUDA(cudaGetLastError());
     return SYM_OK;
@@ -255,10 +502,14 @@ sym_status_t sym_policy_loss_backward(const void* logits, size_t ld, size_t rows
     if (!ctx) return SYM_ERR_CUDA;
     a.status = ctx->status;
     cudaStream_t st = (cudaStream_t)stream;
+    const size_t per = 16 / dtype_size(dtype);
+    const size_t bpr = ceil_div(ceil_div(vocab + per - 1, per), (size_t)(kBackThreads * kBackVectors));
+    if (rows * bpr >= (1ull << 31)) return SYM_ERR_UNSUPPORTED;
+    const unsigned grid = (unsigned)(rows * bpr);
     switch (dtype) {
-        case SYM_F32: k_policy_backward<float><<<(unsigned)rows, kLossThreads, 0, st>>>(a); break;
-        case SYM_BF16: k_policy_backward<__nv_bfloat16><<<(unsigned)rows, kLossThreads, 0, st>>>(a); break;
-        case SYM_F16: k_policy_backward<__half><<<(unsigned)rows, kLossThreads, 0, st>>>(a); break;
+        case SYM_F32: k_policy_backward<float><<<grid, kBackThreads, 0, st>>>(a, (uint32_t)bpr); break;
+        case SYM_BF16: k_policy_backward<__nv_bfloat16><<<grid, kBackThreads, 0, st>>>(a, (uint32_t)bpr); break;
+        case SYM_F16: k_policy_backward<__half><<<grid, kBackThreads, 0, st>>>(a, (uint32_t)bpr); break;
     }
     count_launch();
     SYM_CUDA(cudaGetLastError());

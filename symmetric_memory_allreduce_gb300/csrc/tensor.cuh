@@ -14,6 +14,11 @@ __device__ __forceinline__ uint32_t cluster_rank() {
     return r;
 }
 
+// The cluster barrier in two halves: arrive says that this CTA runs, wait that all do (a CTA's shared
+// memory may be written from outside only then).
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
 // Barrier over all threads of the cluster; orders their shared-memory accesses.
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -33,6 +38,10 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
                  : "r"(addr)
                  : "memory");
     return v;
+}
+
+__device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
