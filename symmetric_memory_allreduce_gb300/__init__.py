@@ -17,7 +17,21 @@ from ._binding import (  # noqa: F401
     SYM_WINDOW_CUDA_MALLOC, SYM_WINDOW_REGISTERED, SYM_WINDOW_VMM, SYM_WINDOW_VMM_EXPORTABLE,
 )
 from ._binding import LIB_PATH  # noqa: F401
-from ._training import (  # noqa: F401
-    AdamW, sym_adamw_step, sym_grad_norm, sym_linear, sym_linear_backward, sym_policy_loss,
-    sym_policy_loss_backward,
-)
+
+# the training operators need torch; they are imported when first asked for
+_TRAINING = ("AdamW", "sym_adamw_step", "sym_grad_norm", "sym_linear", "sym_linear_backward",
+             "sym_policy_loss", "sym_policy_loss_backward")
+
+
+def __getattr__(name):
+    if name in _TRAINING:
+        from . import _training
+
+        for n in _TRAINING:
+            globals()[n] = getattr(_training, n)
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+
+
+def __dir__():
+    return sorted(set(globals()) | set(_TRAINING))

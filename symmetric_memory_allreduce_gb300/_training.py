@@ -7,70 +7,74 @@ from __future__ import annotations
 
 import ctypes
 
-from . import _binding as _b
-from ._binding import ACTS, SymError, _check, _stream
+import torch
 
-_TYPES = {}
+from . import _binding as _b
+from ._binding import ACTS, SymError, _check
+
+_TYPES = {torch.float32: _b.SYM_F32, torch.bfloat16: _b.SYM_BF16, torch.float16: _b.SYM_F16}
+_F32, _I64 = torch.float32, torch.int64
+
+
+def _stream(stream, dev) -> int | None:
+    """cudaStream_t of a torch stream, an int handle, or the device's current torch stream."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev) or None       # the current stream without an object for it
+    return _b._stream(stream)
 
 
 def _type(t) -> int:
     """SYM_* code of a tensor's dtype."""
-    if not _TYPES:
-        import torch
-
-        _TYPES.update({torch.float32: _b.SYM_F32, torch.bfloat16: _b.SYM_BF16, torch.float16: _b.SYM_F16})
-    try:
-        return _TYPES[t.dtype]
-    except KeyError:
-        raise ValueError(f"unsupported dtype {t.dtype}") from None
+    code = _TYPES.get(t.dtype)
+    if code is None:
+        raise ValueError(f"unsupported dtype {t.dtype}")
+    return code
 
 
-def _matrix(t, name, rows, cols, dtype):
-    """(address, row stride) of a rows x cols CUDA tensor with contiguous rows; (None, cols) of None."""
+def _device(t) -> int:
+    """Index of a CUDA tensor's device, which has to be the current one."""
+    d = t.get_device()
+    if d < 0 or d != torch._C._cuda_getDevice():
+        raise ValueError(f"expected tensors on the current CUDA device, got one on {t.device}")
+    return d
+
+
+def _matrix(t, name, rows, cols, dtype, dev):
+    """(address, row stride) of a rows x cols tensor with contiguous rows; (None, cols) of None."""
     if t is None:
         return None, cols
-    if not t.is_cuda or t.dtype != dtype or t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
-        raise ValueError(f"{name}: expected a CUDA {dtype} tensor of shape ({rows}, {cols})")
+    if t.dtype is not dtype or t.get_device() != dev or t.shape != (rows, cols):
+        raise ValueError(f"{name}: expected a {dtype} tensor of shape ({rows}, {cols}) on device {dev}")
     si, sj = t.stride()
     if cols > 1 and sj != 1:
         raise ValueError(f"{name}: the elements of a row must be contiguous")
-    if rows > 1 and si < cols:
-        raise ValueError(f"{name}: rows overlap")
-    return t.data_ptr(), (si if rows > 1 else max(cols, 1))
+    if rows > 1:
+        if si < cols:
+            raise ValueError(f"{name}: rows overlap")
+        return t.data_ptr(), si
+    return t.data_ptr(), max(cols, 1)
 
 
-def _vector(t, name, n, dtype):
-    """Address of a contiguous CUDA tensor of n elements; None of None."""
+def _vector(t, name, n, dtype, dev):
+    """Address of a contiguous tensor of n elements; None of None."""
     if t is None:
         return None
-    if not t.is_cuda or t.dtype != dtype or t.numel() != n or not t.is_contiguous():
-        raise ValueError(f"{name}: expected a contiguous CUDA {dtype} tensor of {n} elements")
+    if t.dtype is not dtype or t.get_device() != dev or t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous {dtype} tensor of {n} elements on device {dev}")
     return t.data_ptr()
-
-
-def _on_one_device(first, *others):
-    d = first.device
-    for t in others:
-        if t is not None and t.device != d:
-            raise ValueError("tensors on different devices")
-    import torch
-
-    if torch.cuda.current_device() != d.index:
-        raise ValueError(f"the tensors' device {d} is not the current one")
 
 
 def _workspace(given, nbytes, like, stream):
     """(address, bytes) of the caller's workspace, or of one from torch's allocator on `stream`."""
     if nbytes == 0:
         return None, 0
-    import torch
-
     if given is None:
         given = torch.empty(nbytes, dtype=torch.uint8, device=like.device)
         if stream is not None:
             # freed on return: the allocator must not hand it out before `stream` is through with it
             given.record_stream(stream if not isinstance(stream, int) else torch.cuda.ExternalStream(stream))
-    elif not given.is_cuda or given.device != like.device or not given.is_contiguous():
+        return given.data_ptr(), nbytes
+    if given.get_device() != like.get_device() or not given.is_contiguous():
         raise ValueError("workspace: expected a contiguous tensor on the inputs' device")
     return given.data_ptr(), given.numel() * given.element_size()
 
@@ -82,17 +86,16 @@ def sym_linear(x, w, y, bias=None, residual=None, pre=None, act="none", workspac
     bfloat16, float16) whose rows are contiguous (any row stride).  act: none, relu, gelu, silu."""
     lib = _b.load()
     (M, K), N, dt = x.shape, w.shape[0], x.dtype
-    code = _type(x)
-    _on_one_device(x, w, y, bias, residual, pre)
-    px, ldx = _matrix(x, "x", M, K, dt)
-    pw, ldw = _matrix(w, "w", N, K, dt)
-    py, ldy = _matrix(y, "y", M, N, dt)
-    pr, ldr = _matrix(residual, "residual", M, N, dt)
-    pp, ldp = _matrix(pre, "pre", M, N, dt)
+    code, dev = _type(x), _device(x)
+    px, ldx = _matrix(x, "x", M, K, dt, dev)
+    pw, ldw = _matrix(w, "w", N, K, dt, dev)
+    py, ldy = _matrix(y, "y", M, N, dt, dev)
+    pr, ldr = _matrix(residual, "residual", M, N, dt, dev)
+    pp, ldp = _matrix(pre, "pre", M, N, dt, dev)
     need = lib.sym_linear_workspace(px, ldx, pw, ldw, M, N, K, code)
     ws, wsb = _workspace(workspace, need, x, stream)
-    _check(lib.sym_linear(px, ldx, pw, ldw, _vector(bias, "bias", N, dt), pr, ldr, py, ldy, pp, ldp, M, N, K, code,
-                          ACTS.get(act, act), ws, wsb, _stream(stream)), "sym_linear")
+    _check(lib.sym_linear(px, ldx, pw, ldw, _vector(bias, "bias", N, dt, dev), pr, ldr, py, ldy, pp, ldp, M, N, K, code,
+                          ACTS.get(act, act), ws, wsb, _stream(stream, dev)), "sym_linear")
 
 
 def sym_linear_backward(dy, x, w, pre=None, dx=None, dw=None, dbias=None, act="none", accumulate=False,
@@ -101,40 +104,34 @@ def sym_linear_backward(dy, x, w, pre=None, dx=None, dw=None, dbias=None, act="n
 
     dw and dbias are of x's dtype or both float32 (e.g. a view of a rank's window), and are added
     to when `accumulate`; any of dx, dw, dbias may be None.  The residual's gradient is dy."""
-    import torch
-
     lib = _b.load()
     (M, K), N, dt = x.shape, w.shape[0], x.dtype
-    code = _type(x)
-    _on_one_device(x, dy, w, pre, dx, dw, dbias)
+    code, dev = _type(x), _device(x)
     gt = dw.dtype if dw is not None else dbias.dtype if dbias is not None else dt
-    if gt != dt and gt != torch.float32:
+    if gt is not dt and gt is not _F32:
         raise ValueError("dw and dbias: expected x's dtype or float32")
     gcode = _TYPES[gt]
-    pdy, lddy = _matrix(dy, "dy", M, N, dt)
-    px, ldx = _matrix(x, "x", M, K, dt)
-    pw, ldw = _matrix(w, "w", N, K, dt)
-    pp, ldp = _matrix(pre, "pre", M, N, dt)
-    pdx, lddx = _matrix(dx, "dx", M, K, dt)
-    pdw, lddw = _matrix(dw, "dw", N, K, gt)
+    pdy, lddy = _matrix(dy, "dy", M, N, dt, dev)
+    px, ldx = _matrix(x, "x", M, K, dt, dev)
+    pw, ldw = _matrix(w, "w", N, K, dt, dev)
+    pp, ldp = _matrix(pre, "pre", M, N, dt, dev)
+    pdx, lddx = _matrix(dx, "dx", M, K, dt, dev)
+    pdw, lddw = _matrix(dw, "dw", N, K, gt, dev)
     a = ACTS.get(act, act)
     need = lib.sym_linear_backward_workspace(pdy, lddy, px, ldx, pw, ldw, M, N, K, code, a)
     ws, wsb = _workspace(workspace, need, x, stream)
     _check(lib.sym_linear_backward(pdy, lddy, px, ldx, pw, ldw, pp, ldp, pdx, lddx, pdw, lddw,
-                                   _vector(dbias, "dbias", N, gt), M, N, K, code, gcode, a, int(bool(accumulate)),
-                                   ws, wsb, _stream(stream)), "sym_linear_backward")
+                                   _vector(dbias, "dbias", N, gt, dev), M, N, K, code, gcode, a, int(bool(accumulate)),
+                                   ws, wsb, _stream(stream, dev)), "sym_linear_backward")
 
 
 def _policy_args(logits, targets, old_logp, ref_logp, advantages, weights):
-    import torch
-
     T, V = logits.shape
-    f = torch.float32
-    _on_one_device(logits, targets, old_logp, ref_logp, advantages, weights)
-    p, ld = _matrix(logits, "logits", T, V, logits.dtype)
-    return T, V, f, (p, ld, T, V, _type(logits), _vector(targets, "targets", T, torch.int64),
-                     _vector(old_logp, "old_logp", T, f), _vector(ref_logp, "ref_logp", T, f),
-                     _vector(advantages, "advantages", T, f), _vector(weights, "weights", T, f))
+    dev = _device(logits)
+    p, ld = _matrix(logits, "logits", T, V, logits.dtype, dev)
+    return T, V, dev, (p, ld, T, V, _type(logits), _vector(targets, "targets", T, _I64, dev),
+                       _vector(old_logp, "old_logp", T, _F32, dev), _vector(ref_logp, "ref_logp", T, _F32, dev),
+                       _vector(advantages, "advantages", T, _F32, dev), _vector(weights, "weights", T, _F32, dev))
 
 
 def sym_policy_loss(logits, targets, old_logp, advantages, weights, stats, logp, lse, ref_logp=None, dlogits=None,
@@ -145,24 +142,22 @@ def sym_policy_loss(logits, targets, old_logp, advantages, weights, stats, logp,
     be None); outputs stats (4), logp (T), lse (T) float32, and with `dlogits` (T, V) the gradient in
     the same pass (it may be `logits` itself), times the device scalar `grad_out` if given."""
     lib = _b.load()
-    T, V, f, head = _policy_args(logits, targets, old_logp, ref_logp, advantages, weights)
-    _on_one_device(logits, stats, logp, lse, dlogits, grad_out)
-    pd, ldd = _matrix(dlogits, "dlogits", T, V, logits.dtype)
-    _check(lib.sym_policy_loss(*head, clip_low, clip_high, kl_coef, temperature, _vector(stats, "stats", 4, f),
-                               _vector(logp, "logp", T, f), _vector(lse, "lse", T, f), pd, ldd,
-                               _vector(grad_out, "grad_out", 1, f), _stream(stream)), "sym_policy_loss")
+    T, V, dev, head = _policy_args(logits, targets, old_logp, ref_logp, advantages, weights)
+    pd, ldd = _matrix(dlogits, "dlogits", T, V, logits.dtype, dev)
+    _check(lib.sym_policy_loss(*head, clip_low, clip_high, kl_coef, temperature, _vector(stats, "stats", 4, _F32, dev),
+                               _vector(logp, "logp", T, _F32, dev), _vector(lse, "lse", T, _F32, dev), pd, ldd,
+                               _vector(grad_out, "grad_out", 1, _F32, dev), _stream(stream, dev)), "sym_policy_loss")
 
 
 def sym_policy_loss_backward(logits, targets, old_logp, advantages, weights, logp, lse, dlogits, ref_logp=None,
                              clip_low=0.2, clip_high=0.2, kl_coef=0.0, temperature=1.0, grad_out=None, stream=None):
     """dlogits from the logp and lse that sym_policy_loss left, with the same other arguments."""
     lib = _b.load()
-    T, V, f, head = _policy_args(logits, targets, old_logp, ref_logp, advantages, weights)
-    _on_one_device(logits, logp, lse, dlogits, grad_out)
-    pd, ldd = _matrix(dlogits, "dlogits", T, V, logits.dtype)
+    T, V, dev, head = _policy_args(logits, targets, old_logp, ref_logp, advantages, weights)
+    pd, ldd = _matrix(dlogits, "dlogits", T, V, logits.dtype, dev)
     _check(lib.sym_policy_loss_backward(*head, clip_low, clip_high, kl_coef, temperature,
-                                        _vector(logp, "logp", T, f), _vector(lse, "lse", T, f), pd, ldd,
-                                        _vector(grad_out, "grad_out", 1, f), _stream(stream)),
+                                        _vector(logp, "logp", T, _F32, dev), _vector(lse, "lse", T, _F32, dev), pd, ldd,
+                                        _vector(grad_out, "grad_out", 1, _F32, dev), _stream(stream, dev)),
            "sym_policy_loss_backward")
 
 
@@ -174,8 +169,6 @@ class AdamW:
     tensors are kept alive by this object and must not move (views of a window's memory do not)."""
 
     def __init__(self, params, grads, m, v, m_scales=None, v_scales=None, copies=None):
-        import torch
-
         lib = _b.load()
         self.handle = None
         n = len(params)
@@ -196,11 +189,10 @@ class AdamW:
         ct = copies[0].dtype if copies else torch.float32
         for t in (params[:1] + grads[:1] + (copies or [])[:1]):
             _type(t)
-        if n:
-            _on_one_device(params[0], *[t for _, ts in [("", params)] + lists for t in ts])
+        self.device = dev = _device(params[0]) if n else torch.cuda.current_device()
 
         def addresses(name, ts, sizes, dtype):
-            return (ctypes.c_void_p * max(n, 1))(*[_vector(t, f"{name}[{i}]", sizes[i], dtype)
+            return (ctypes.c_void_p * max(n, 1))(*[_vector(t, f"{name}[{i}]", sizes[i], dtype, dev)
                                                    for i, t in enumerate(ts)])
 
         out = ctypes.c_void_p()
@@ -236,18 +228,12 @@ class AdamW:
 def sym_adamw_step(plan, lr, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.0, step=1, grad_scale=None, seed=0,
                    stream=None):
     """One step in place; grad_scale: a device float32 scalar (sym_grad_norm's second output, say)."""
-    gs = None
-    if grad_scale is not None:
-        import torch
-
-        gs = _vector(grad_scale, "grad_scale", 1, torch.float32)
+    gs = _vector(grad_scale, "grad_scale", 1, _F32, plan.device)
     _check(_b.load().sym_adamw_step(plan.handle, lr, beta1, beta2, eps, weight_decay, step, gs, seed & 0xFFFFFFFF,
-                                    _stream(stream)), "sym_adamw_step")
+                                    _stream(stream, plan.device)), "sym_adamw_step")
 
 
 def sym_grad_norm(plan, out, max_norm, stream=None):
     """out (2 float32): the norm of all gradients, and the factor that clips them to max_norm."""
-    import torch
-
-    _check(_b.load().sym_grad_norm(plan.handle, max_norm, _vector(out, "out", 2, torch.float32), _stream(stream)),
-           "sym_grad_norm")
+    _check(_b.load().sym_grad_norm(plan.handle, max_norm, _vector(out, "out", 2, _F32, plan.device),
+                                   _stream(stream, plan.device)), "sym_grad_norm")

@@ -89,32 +89,6 @@ __device__ __forceinline__ float pow2i(int e) {
     return __uint_as_float(e == -127 ? 0x00400000u : (uint32_t)(e + 127) << 23);
 }
 
-// Two binary32 operations per instruction, each rounded once (no contraction across them).
-struct F2 {
-    uint64_t v;
-};
-__device__ __forceinline__ F2 f2(float x, float y) {
-    F2 r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(x), "f"(y));
-    return r;
-}
-__device__ __forceinline__ void split(F2 a, float& x, float& y) {
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(a.v));
-}
-// a*b + z with z = (-0, -0) is a*b rounded once, signs of zero included.  z is a kernel argument: a
-// packed product the compiler can see is contracted with the sum that follows it (measured: other
-// bits than mul and add apart).
-__device__ __forceinline__ F2 mul2(F2 a, F2 b, F2 z) {
-    F2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(z.v));
-    return r;
-}
-__device__ __forceinline__ F2 add2(F2 a, F2 b) {
-    F2 r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-    return r;
-}
-
 struct AdamArgs {
     const AdamTensor* tensors;
     const AdamChunk* chunks;
@@ -511,23 +485,23 @@ __global__ void __launch_bounds__(kAdamThreads)
         }
         ++k;
     }
-    __shared__ double red[kAdamThreads / 32];
+    __shared__ float red[kAdamThreads / 32];
     __shared__ bool last;
-    double d = block_sum<kAdamThreads>((double)s, red);
+    s = block_sum<kAdamThreads>(s, red);
     if (threadIdx.x == 0) {
-        partial[blockIdx.x] = (float)d;
+        partial[blockIdx.x] = s;
         __threadfence();
         last = atomicAdd(counter, 1u) == gridDim.x - 1;
     }
     __syncthreads();
     if (!last) return;
     __threadfence();
-    double t = 0.;
-    for (uint32_t i = threadIdx.x; i < gridDim.x; i += kAdamThreads) t += (double)__ldcg(partial + i);
+    float t = 0.f;
+    for (uint32_t i = threadIdx.x; i < gridDim.x; i += kAdamThreads) t += __ldcg(partial + i);
     t = block_sum<kAdamThreads>(t, red);
     if (threadIdx.x == 0) {
         *counter = 0;
-        const float norm = (float)sqrt(t);
+        const float norm = sqrtf(t);
         out[0] = norm;
         out[1] = isfinite(norm) ? fminf(1.f, __fdiv_rn(max_norm, __fadd_rn(norm, 1e-6f))) : nanf("");
     }

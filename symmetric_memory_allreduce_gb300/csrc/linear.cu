@@ -4,7 +4,11 @@
 //   forward   Y = act(X W^T + b) + R            (Z = X W^T + b kept if asked)
 //   backward  dZ = dY * act'(Z),  dX = dZ W,  dW = dZ^T X,  db = sum_m dZ
 // X is M x K, W is N x K, Y is M x N, all with rows of contiguous elements.
+#include <cmath>
+#include <cstdlib>
+
 #include "linear.cuh"
+#include "tensor.cuh"
 
 namespace symar {
 
@@ -12,10 +16,12 @@ namespace symar {
 //
 // One pass over dY (and Z): writes dZ rounded to the inputs' type (the tensor
 // cores' operand type; the products that follow sum in 32 bits) and sums its
-// columns unrounded in 32 bits.  A block takes 256 columns of a strip of rows;
-// the strips' sums are added in order by a second launch.
+// columns unrounded in 32 bits.  A cluster of 8 blocks takes 64 columns, each
+// block an eighth of the rows; the first adds the eight sums in order through
+// their shared memory, so the bias's gradient needs no scratch and no second
+// launch and is the same bits every time.
 
-constexpr int kDzThreads = 256, kDzCols = 256, kDzVec = 8;
+constexpr int kDzThreads = 256, kDzCols = 64, kDzCluster = 8, kDzUnroll = 4;
 
 struct DzArgs {
     const void* dy;
@@ -24,57 +30,98 @@ struct DzArgs {
     size_t ldp;
     void* dz;              // null: not wanted
     size_t ldz;
-    float* partial;        // [strips][N]; null: not wanted
-    size_t M, N, strip;
+    void* db;              // null: not wanted
+    size_t M, N;
     int act;
+    bool accumulate, vec;  // vec: every row of dy, pre and dz starts at a 16-byte boundary
 };
 
 template <class X>
-__global__ void __launch_bounds__(kDzThreads) k_linear_dz(DzArgs a) {
-    constexpr int LANES = kDzCols / kDzVec, ROWS = kDzThreads / LANES;
-    __shared__ float red[ROWS][kDzCols];
-    const int tx = threadIdx.x % LANES, ty = threadIdx.x / LANES;
-    const size_t j0 = (size_t)blockIdx.x * kDzCols + tx * kDzVec;
-    const size_t r0 = (size_t)blockIdx.y * a.strip, r1 = min(r0 + a.strip, a.M);
-    float s[kDzVec] = {};
-    for (size_t i = r0 + ty; i < r1; i += ROWS) {
+__device__ __forceinline__ void load_row(const void* p, size_t at, int live, bool vec, float (&f)[8]) {
+    const X* q = static_cast<const X*>(p) + at;
+    if (vec && live == 8) {
+        uint4 v[sizeof(X) / 2];
 #pragma unroll
-        for (int e = 0; e < kDzVec; ++e) {
-            const size_t j = j0 + e;
-            if (j >= a.N) break;
-            float d = load_f<X>(a.dy, i * a.ldy + j);
-            if (a.pre) d *= act_slope(load_f<X>(a.pre, i * a.ldp + j), a.act);
-            s[e] += d;
-            if (a.dz) store_f<X>(a.dz, i * a.ldz + j, d);
+        for (int k = 0; k < (int)sizeof(X) / 2; ++k) v[k] = __ldcs(reinterpret_cast<const uint4*>(q) + k);
+        const X* h = reinterpret_cast<const X*>(v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] = to_f(h[e]);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[e] = e < live ? to_f(q[e]) : 0.f;
+    }
+}
+
+template <class X>
+__device__ __forceinline__ void store_row(void* p, size_t at, int live, bool vec, const float (&f)[8]) {
+    X* q = static_cast<X*>(p) + at;
+    if (vec && live == 8) {
+        uint4 v[sizeof(X) / 2];
+        X* h = reinterpret_cast<X*>(v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) h[e] = from_f<X>(f[e]);
+#pragma unroll
+        for (int k = 0; k < (int)sizeof(X) / 2; ++k) reinterpret_cast<uint4*>(q)[k] = v[k];
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (e < live) q[e] = from_f<X>(f[e]);
+    }
+}
+
+template <class X, class O>
+__global__ void __launch_bounds__(kDzThreads) k_linear_dz(DzArgs a) {
+    constexpr int LANES = kDzCols / 8, ROWS = kDzThreads / LANES;
+    __shared__ float red[ROWS][kDzCols + 4];
+    __shared__ float sums[kDzCluster][kDzCols];              // the first block's: every block's sums
+    const uint32_t rank = cluster_rank();
+    const int tx = threadIdx.x % LANES, ty = threadIdx.x / LANES;
+    const size_t j0 = (size_t)(blockIdx.x / kDzCluster) * kDzCols, j = j0 + tx * 8;
+    const int live = j < a.N ? (int)min((size_t)8, a.N - j) : 0;
+    const size_t strip = (a.M + kDzCluster - 1) / kDzCluster;
+    const size_t r0 = rank * strip, r1 = min(r0 + strip, a.M);
+    cluster_arrive();                                        // waited for before the first remote store
+    float s[8] = {};
+    for (size_t i = r0 + ty; live && i < r1; i += (size_t)ROWS * kDzUnroll) {
+        float d[kDzUnroll][8], z[kDzUnroll][8];
+#pragma unroll
+        for (int u = 0; u < kDzUnroll; ++u) {
+            const size_t r = i + (size_t)u * ROWS;
+            if (r >= r1) continue;
+            load_row<X>(a.dy, r * a.ldy + j, live, a.vec, d[u]);
+            if (a.pre) load_row<X>(a.pre, r * a.ldp + j, live, a.vec, z[u]);
+        }
+#pragma unroll
+        for (int u = 0; u < kDzUnroll; ++u) {
+            const size_t r = i + (size_t)u * ROWS;
+            if (r >= r1) continue;
+            if (a.pre) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) d[u][e] *= act_slope(z[u][e], a.act);
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s[e] += d[u][e];
+            if (a.dz) store_row<X>(a.dz, r * a.ldz + j, live, a.vec, d[u]);
         }
     }
-    if (!a.partial) return;
 #pragma unroll
-    for (int e = 0; e < kDzVec; ++e) red[ty][tx * kDzVec + e] = s[e];
+    for (int e = 0; e < 8; ++e) red[ty][tx * 8 + e] = s[e];
     __syncthreads();
-    const size_t j = (size_t)blockIdx.x * kDzCols + threadIdx.x;
-    if (j >= a.N) return;
-    float t = 0.f;
+    cluster_wait();
+    if (a.db && threadIdx.x < kDzCols) {
+        float t = 0.f;
 #pragma unroll
-    for (int r = 0; r < ROWS; ++r) t += red[r][threadIdx.x];
-    a.partial[(size_t)blockIdx.y * a.N + j] = t;
-}
-
-template <class O>
-__global__ void __launch_bounds__(kDzThreads) k_linear_db(const float* partial, size_t strips, size_t N, void* db,
-                                                          bool accumulate) {
-    const size_t j = (size_t)blockIdx.x * kDzThreads + threadIdx.x;
-    if (j >= N) return;
-    float t = accumulate ? load_f<O>(db, j) : 0.f;
-    for (size_t s = 0; s < strips; ++s) t += partial[s * N + j];
-    store_f<O>(db, j, t);
-}
-
-// Rows per strip: about four blocks per SM over all strips, at least 32 rows each.
-static size_t dz_strip(size_t M, size_t N) {
-    const size_t cols = ceil_div(N, (size_t)kDzCols);
-    const size_t strips = std::max<size_t>(1, std::min<size_t>(ceil_div((size_t)608, cols), ceil_div(M, (size_t)32)));
-    return std::max<size_t>(1, ceil_div(M, strips));
+        for (int r = 0; r < ROWS; ++r) t += red[r][threadIdx.x];
+        st_cluster_f32(map_rank(smem_u32(&sums[rank][threadIdx.x]), 0), t);
+    }
+    __syncwarp();
+    cluster_sync();
+    if (a.db && rank == 0 && threadIdx.x < kDzCols && j0 + threadIdx.x < a.N) {
+        float t = a.accumulate ? load_f<O>(a.db, j0 + threadIdx.x) : 0.f;
+#pragma unroll
+        for (int r = 0; r < kDzCluster; ++r) t += sums[r][threadIdx.x];
+        store_f<O>(a.db, j0 + threadIdx.x, t);
+    }
 }
 
 // ---------------------------------------------------------------- unaligned operands
@@ -127,20 +174,9 @@ static sym_status_t align_operand(const void*& p, size_t& ld, size_t rows, size_
     return SYM_OK;
 }
 
-struct BackwardPlan {
-    size_t strip, strips, ldz, dz_off, partial_off, align_off, bytes;
-};
-
-static BackwardPlan backward_plan(size_t M, size_t N, size_t es, int act, size_t aligned) {
-    BackwardPlan p{};
-    p.strip = dz_strip(M, N);
-    p.strips = std::max<size_t>(1, ceil_div(M, p.strip));
-    p.ldz = ceil_div(N, (size_t)8) * 8;
-    const size_t dz = act == SYM_ACT_NONE ? 0 : ceil_div(M * p.ldz * es, (size_t)256) * 256;
-    p.partial_off = p.dz_off + dz;
-    p.align_off = p.partial_off + ceil_div(p.strips * N * sizeof(float), (size_t)256) * 256;
-    p.bytes = p.align_off + aligned;
-    return p;
+// Workspace of the backward call: dZ (rows padded to 16 bytes), then aligned operands.
+static size_t dz_bytes(size_t M, size_t N, size_t es, int act) {
+    return act == SYM_ACT_NONE ? 0 : ceil_div(M * padded(N) * es, (size_t)256) * 256;
 }
 
 static bool good_act(int act) { return act >= SYM_ACT_NONE && act <= SYM_ACT_SILU; }
@@ -155,15 +191,41 @@ static Span span(const void* p, size_t rows, size_t n, size_t ld, size_t es) {
 }
 static bool meet(Span x, Span y) { return x.a < y.b && y.a < x.b; }
 
+// Tile rows and k shares of a tensor-core product: the least of an estimate in clocks.  A pair's step of
+// 64 k takes the longer of its four instructions (2 NT clocks) and of its copies (32 + NT/8 KB for the
+// pair at about 64 bytes a clock and SM); a tile's epilogue about 12 clocks a row and runs under the next tile's
+// steps; sharing k out costs a cluster's exchange.
+static void tc_shape(const MatmulArgs& m, bool b_mn, int num_sms, int* nt_out, uint32_t* splits_out) {
+    const double kblocks = (double)ceil_div(m.kk, (size_t)64), tj = (double)ceil_div(m.n, (size_t)256);
+    double best = 1e300;
+    for (int nt = b_mn ? 128 : 16; nt <= 256; nt *= 2) {
+        const double tiles = tj * (double)ceil_div(m.m, (size_t)nt);
+        for (uint32_t s = 1; s <= 4; s *= 2) {
+            if (s > 1 && (kblocks < 4 * s || nt > 128)) continue;
+            const double step = std::max(2.0 * nt, 256.0 + nt), main = std::ceil(kblocks / s) * step;
+            const double epi = 12.0 * std::min<double>(nt, (double)m.m) / (s > 1 ? s : 1) + (s > 1 ? 2500 : 0);
+            const double waves = std::ceil(tiles * s / (num_sms / 2));
+            const double t = waves * std::max(main, s > 1 ? main + epi : epi) + (s > 1 ? 0 : epi);
+            if (t < best) best = t, *nt_out = nt, *splits_out = s;
+        }
+    }
+#ifdef TC_SWEEP
+    if (getenv("TC_NT")) *nt_out = atoi(getenv("TC_NT")), *splits_out = atoi(getenv("TC_S"));
+#endif
+}
+
 // out = a b^T on the units of its type.  a_mn, b_mn: which index the operands are contiguous along
 // (matmul_tc_bf16).  Without terms (kk = 0) the FMA kernel writes the epilogue of zero.
 static sym_status_t matmul(const MatmulArgs& m, sym_dtype_t in, sym_dtype_t out, bool a_mn, bool b_mn,
                            cudaStream_t st) {
     if (in == SYM_F32 || m.kk == 0) return matmul_simt(m, in, out, st);
+    int dev = 0;
+    SYM_CUDA(cudaGetDevice(&dev));
+    DevCtx* ctx = dev_ctx(dev);
+    if (!ctx) return SYM_ERR_CUDA;
     int nt = 256;
-    if (b_mn) nt = m.m <= 128 ? 128 : 256;
-    else while (nt > 16 && m.m <= (size_t)nt / 2) nt /= 2;
-    const uint32_t splits = 1;
+    uint32_t splits = 1;
+    tc_shape(m, b_mn, ctx->num_sms, &nt, &splits);
     return in == SYM_BF16 ? matmul_tc_bf16(m, out, a_mn, b_mn, nt, splits, st)
                           : matmul_tc_f16(m, out, a_mn, b_mn, nt, splits, st);
 }
@@ -225,9 +287,9 @@ sym_status_t sym_linear(const void* x, size_t ldx, const void* w, size_t ldw, co
 
 size_t sym_linear_backward_workspace(const void* dy, size_t lddy, const void* x, size_t ldx, const void* w, size_t ldw,
                                      size_t M, size_t N, size_t K, sym_dtype_t dtype, sym_act_t act) {
-    const size_t aligned = (act == SYM_ACT_NONE ? align_bytes(dy, M, N, lddy, dtype) : 0) +
-                           align_bytes(x, M, K, ldx, dtype) + align_bytes(w, N, K, ldw, dtype);
-    return backward_plan(M, N, dtype_size(dtype), act, aligned).bytes;
+    return dz_bytes(M, N, dtype_size(dtype), act) +
+           (act == SYM_ACT_NONE ? align_bytes(dy, M, N, lddy, dtype) : 0) + align_bytes(x, M, K, ldx, dtype) +
+           align_bytes(w, N, K, ldw, dtype);
 }
 
 sym_status_t sym_linear_backward(const void* dy, size_t lddy, const void* x, size_t ldx, const void* w, size_t ldw,
@@ -247,16 +309,13 @@ sym_status_t sym_linear_backward(const void* dy, size_t lddy, const void* x, siz
     for (const void* p : {dy, x, w, pre, (const void*)dx})
         if ((uintptr_t)p % es) return SYM_ERR_INVALID_ARG;
     if ((uintptr_t)dw % gs || (uintptr_t)dbias % gs) return SYM_ERR_INVALID_ARG;
-    const BackwardPlan bp =
-        backward_plan(M, N, es, act,
-                      sym_linear_backward_workspace(dy, lddy, x, ldx, w, ldw, M, N, K, dtype, act) -
-                          backward_plan(M, N, es, act, 0).bytes);
-    if (workspace_bytes < bp.bytes || (!workspace && bp.bytes) || (uintptr_t)workspace % 256) {
+    const size_t need = sym_linear_backward_workspace(dy, lddy, x, ldx, w, ldw, M, N, K, dtype, act);
+    if (workspace_bytes < need || (!workspace && workspace_bytes) || (uintptr_t)workspace % 256) {
         set_last_error("sym_linear_backward: workspace missing, too small or not 256-byte aligned");
         return SYM_ERR_INVALID_ARG;
     }
     const Span outs[] = {span(dx, M, K, lddx, es), span(dw, N, K, lddw, gs), span(dbias, 1, N, N, gs),
-                         span(workspace, 1, bp.bytes, bp.bytes, 1)};
+                         span(workspace, 1, need, need, 1)};
     const Span ins[] = {span(dy, M, N, lddy, es), span(x, M, K, ldx, es), span(w, N, K, ldw, es),
                         span(pre, M, N, ldp, es)};
     for (int i = 0; i < 4; ++i) {
@@ -275,43 +334,41 @@ sym_status_t sym_linear_backward(const void* dy, size_t lddy, const void* x, siz
     char* ws = (char*)workspace;
     const void* dz = dy;
     size_t lddz = lddy;
-    if (N && M && (act != SYM_ACT_NONE || dbias)) {
-        DzArgs d{dy, lddy, act == SYM_ACT_NONE ? nullptr : pre, ldp, nullptr, 0, nullptr, M, N, bp.strip, (int)act};
+    if (N && (act != SYM_ACT_NONE || dbias)) {
+        DzArgs d{dy, lddy, act == SYM_ACT_NONE ? nullptr : pre, ldp, nullptr, 0, dbias, M, N, (int)act,
+                 accumulate != 0, false};
         if (act != SYM_ACT_NONE && (dx || dw)) {
-            d.dz = ws + bp.dz_off;
-            d.ldz = bp.ldz;
+            d.dz = ws;
+            d.ldz = padded(N);
             dz = d.dz;
-            lddz = bp.ldz;
+            lddz = d.ldz;
         }
-        if (dbias) d.partial = (float*)(ws + bp.partial_off);
-        const dim3 grid((unsigned)ceil_div(N, (size_t)kDzCols), (unsigned)bp.strips);
+        const size_t row = 16 / es;
+        d.vec = (uintptr_t)dy % 16 == 0 && lddy % row == 0 &&
+                (!d.pre || ((uintptr_t)pre % 16 == 0 && ldp % row == 0));
+        const void* k = nullptr;
         switch (dtype) {
-            case SYM_F32: k_linear_dz<float><<<grid, kDzThreads, 0, st>>>(d); break;
-            case SYM_BF16: k_linear_dz<__nv_bfloat16><<<grid, kDzThreads, 0, st>>>(d); break;
-            case SYM_F16: k_linear_dz<__half><<<grid, kDzThreads, 0, st>>>(d); break;
+            case SYM_F32: k = (const void*)k_linear_dz<float, float>; break;
+            case SYM_BF16: k = grad_dtype == SYM_F32 ? (const void*)k_linear_dz<__nv_bfloat16, float>
+                                                     : (const void*)k_linear_dz<__nv_bfloat16, __nv_bfloat16>; break;
+            case SYM_F16: k = grad_dtype == SYM_F32 ? (const void*)k_linear_dz<__half, float>
+                                                    : (const void*)k_linear_dz<__half, __half>; break;
         }
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3((unsigned)(ceil_div(N, (size_t)kDzCols) * kDzCluster));
+        cfg.blockDim = dim3(kDzThreads);
+        cfg.stream = st;
+        cudaLaunchAttribute attr{};
+        attr.id = cudaLaunchAttributeClusterDimension;
+        attr.val.clusterDim.x = kDzCluster;
+        attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+        void* args[] = {&d};
+        SYM_CUDA(cudaLaunchKernelExC(&cfg, k, args));
         count_launch();
-        SYM_CUDA(cudaGetLastError());
     }
-    if (dbias && N) {
-        const unsigned grid = (unsigned)ceil_div(N, (size_t)kDzThreads);
-        const float* partial = (const float*)(ws + bp.partial_off);
-        const size_t strips = M ? bp.strips : 0;
-        switch (grad_dtype) {
-            case SYM_F32:
-                k_linear_db<float><<<grid, kDzThreads, 0, st>>>(partial, strips, N, dbias, accumulate != 0);
-                break;
-            case SYM_BF16:
-                k_linear_db<__nv_bfloat16><<<grid, kDzThreads, 0, st>>>(partial, strips, N, dbias, accumulate != 0);
-                break;
-            case SYM_F16:
-                k_linear_db<__half><<<grid, kDzThreads, 0, st>>>(partial, strips, N, dbias, accumulate != 0);
-                break;
-        }
-        count_launch();
-        SYM_CUDA(cudaGetLastError());
-    }
-    char* at = ws + bp.align_off;
+    char* at = ws + dz_bytes(M, N, es, act);
     if ((dx && M && K) || (dw && N && K)) {
         sym_status_t s = SYM_OK;
         if (N && M && dz == dy) s = align_operand(dz, lddz, M, N, dtype, at, st);

@@ -116,73 +116,92 @@ struct Quad<__half> {
     }
 };
 
-// Four elements from or to a row, by one access when `vec`, of which `live` (1..4) exist.
-template <class T>
-__device__ __forceinline__ void load4(const void* p, size_t at, bool vec, int live, float (&f)[4]) {
-    const T* q = static_cast<const T*>(p) + at;
-    if (vec) {
-        Quad<T>::get(*reinterpret_cast<const typename Quad<T>::V*>(q), f);
-    } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) f[e] = e < live ? to_f(q[e]) : 0.f;
-    }
-}
-template <class T>
-__device__ __forceinline__ void store4(void* p, size_t at, bool vec, int live, const float (&f)[4]) {
-    T* q = static_cast<T*>(p) + at;
-    if (vec) {
-        *reinterpret_cast<typename Quad<T>::V*>(q) = Quad<T>::put(f);
-    } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            if (e < live) q[e] = from_f<T>(f[e]);
-    }
-}
-
-// What one lane's four columns share over all rows of a tile.
-template <class X, class O>
+// The epilogue of one lane: R rows of a tile, four columns of each.  VEC: four neighbouring ones, by
+// accesses of four elements (every row of the output and of what is read with it starts at such a
+// boundary and the columns come in fours); else columns 32 apart, so that a warp's accesses of single
+// elements are still contiguous.
+template <class X, class O, bool VEC>
 struct TcColumns {
+    static constexpr int STEP = VEC ? 1 : 32;
     size_t j;
-    int live;                 // columns that exist (0: none)
-    bool vec_o, vec_r, vec_p;
+    int live;                 // of columns j, j + STEP, ... those that exist
     float bias[4];
 
-    __device__ __forceinline__ void set(const MatmulArgs& m, size_t j_) {
-        j = j_;
-        live = j < m.n ? (int)min((size_t)4, m.n - j) : 0;
-        const bool four = live == 4;
-        vec_o = four && m.ldo % 4 == 0 && (uintptr_t)m.out % (4 * sizeof(O)) == 0;
-        vec_r = four && m.ldr % 4 == 0 && (uintptr_t)m.residual % (4 * sizeof(X)) == 0;
-        vec_p = four && m.ldp % 4 == 0 && (uintptr_t)m.pre % (4 * sizeof(X)) == 0;
-        if (m.bias && live) load4<X>(m.bias, j, false, live, bias);
-        else bias[0] = bias[1] = bias[2] = bias[3] = 0.f;
+    __device__ __forceinline__ void set(const MatmulArgs& m, size_t j0, int lane) {
+        j = j0 + (VEC ? lane * 4 : lane);
+        live = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            bias[e] = 0.f;
+            if (j + e * STEP < m.n) {
+                live = e + 1;
+                if (m.bias) bias[e] = load_f<X>(m.bias, j + e * STEP);
+            }
+        }
     }
 
-    __device__ __forceinline__ void finish(const MatmulArgs& m, size_t i, float4 sum) const {
-        float z[4] = {sum.x + bias[0], sum.y + bias[1], sum.z + bias[2], sum.w + bias[3]};
-        if (m.pre) store4<X>(m.pre, i * m.ldp + j, vec_p, live, z);
+    // Where the lane's four sums of a 128-column row are in shared memory.
+    static __device__ __forceinline__ float4 sums(const float* row, int lane) {
+        if (VEC) return *reinterpret_cast<const float4*>(row + lane * 4);
+        return make_float4(row[lane], row[lane + 32], row[lane + 64], row[lane + 96]);
+    }
+
+    template <class T, int R>
+    struct Rows {
+        typename Quad<T>::V v[VEC ? R : 1];
+        T e[VEC ? 1 : R][4];
+
+        __device__ __forceinline__ void load(const TcColumns& c, const void* p, size_t ld, size_t i0, size_t m) {
+            const T* q = static_cast<const T*>(p) + i0 * ld + c.j;
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                if (i0 + r >= m || !c.live) continue;
+                if (VEC) {
+                    v[r] = *reinterpret_cast<const typename Quad<T>::V*>(q + r * ld);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        if (k < c.live) e[r][k] = q[r * ld + k * 32];
+                }
+            }
+        }
+        __device__ __forceinline__ void add(int r, int live, float (&z)[4]) const {
+            float f[4];
+            if (VEC) {
+                Quad<T>::get(v[r], f);
+            } else {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) f[k] = k < live ? to_f(e[r][k]) : 0.f;
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) z[k] += f[k];
+        }
+    };
+
+    template <class T>
+    __device__ __forceinline__ void store(void* p, size_t at, const float (&z)[4]) const {
+        T* q = static_cast<T*>(p) + at + j;
+        if (VEC) {
+            *reinterpret_cast<typename Quad<T>::V*>(q) = Quad<T>::put(z);
+        } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (k < live) q[k * 32] = from_f<T>(z[k]);
+        }
+    }
+
+    __device__ __forceinline__ void activate(const MatmulArgs& m, size_t i, float4 sum, float (&z)[4]) const {
+        z[0] = sum.x + bias[0], z[1] = sum.y + bias[1], z[2] = sum.z + bias[2], z[3] = sum.w + bias[3];
+        if (m.pre) store<X>(m.pre, i * m.ldp, z);
         if (m.act != SYM_ACT_NONE) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) z[e] = act_value(z[e], m.act);
         }
-        if (m.residual) {
-            float r[4];
-            load4<X>(m.residual, i * m.ldr + j, vec_r, live, r);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) z[e] += r[e];
-        }
-        if (m.accumulate) {
-            float r[4];
-            load4<O>(m.out, i * m.ldo + j, vec_o, live, r);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) z[e] += r[e];
-        }
-        store4<O>(m.out, i * m.ldo + j, vec_o, live, z);
     }
 };
 
 // A_MN / B_MN: the operand's contiguous index is j / i (else k).
-template <class X, class O, bool A_MN, bool B_MN, int NT>
+template <class X, class O, bool A_MN, bool B_MN, int NT, bool VEC>
 __global__ void __launch_bounds__(kTcThreads, 1) k_matmul_tc(const __grid_constant__ TcArgs a) {
     constexpr int STAGES = tc_stages(NT), CW = NT < 32 ? NT : 32, CHUNKS = NT / CW;
     constexpr int GROUPS = CHUNKS > 1 ? 2 : 1;                       // epilogue groups of 4 warps at work
@@ -292,10 +311,16 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_matmul_tc(const __grid_consta
             const bool late = !tc_wait(&s->acc_full[buf], n >> 1 & 1, a, s, 4);
             if (named_any(1 + g, 128, late)) break;                  // the group's threads agree: no barrier is left open
             tc_fence_after();
-            TcColumns<X, O> col;
-            col.set(a.m, (size_t)tj * 256 + half * 128 + lane * 4);
+            TcColumns<X, O, VEC> col;
+            col.set(a.m, (size_t)tj * 256 + half * 128, lane);
 #pragma unroll 1
             for (int c = g; c < CHUNKS; c += GROUPS) {
+                constexpr int R = CW / 4;                            // rows of the piece that this warp finishes
+                const size_t i0 = (size_t)ti * NT + c * CW + q * R;
+                typename TcColumns<X, O, VEC>::template Rows<X, R> res;
+                typename TcColumns<X, O, VEC>::template Rows<O, R> old;
+                if (a.m.residual) res.load(col, a.m.residual, a.m.ldr, i0, a.m.m);
+                if (a.m.accumulate) old.load(col, a.m.out, a.m.ldo, i0, a.m.m);
                 float v[CW];
                 tmem_load(tmem + buf * NT + c * CW + ((uint32_t)(q * 32) << 16), v);
                 if (c + GROUPS >= CHUNKS) {
@@ -306,11 +331,16 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_matmul_tc(const __grid_consta
 #pragma unroll
                 for (int r = 0; r < CW; ++r) stage[r * 128 + q * 32 + lane] = v[r];
                 named_sync(1 + g, 128);
-                const size_t i0 = (size_t)ti * NT + c * CW + q * (CW / 4);
-#pragma unroll 4
-                for (int r = 0; r < CW / 4; ++r) {
-                    const float4 z = *reinterpret_cast<const float4*>(stage + (q * (CW / 4) + r) * 128 + lane * 4);
-                    if (i0 + r < a.m.m && col.live) col.finish(a.m, i0 + r, z);
+                if (col.live) {
+#pragma unroll
+                    for (int r = 0; r < R; ++r) {
+                        if (i0 + r >= a.m.m) break;
+                        float z[4];
+                        col.activate(a.m, i0 + r, col.sums(stage + (q * R + r) * 128, lane), z);
+                        if (a.m.residual) res.add(r, col.live, z);
+                        if (a.m.accumulate) old.add(r, col.live, z);
+                        col.template store<O>(a.m.out, (i0 + r) * a.m.ldo, z);
+                    }
                 }
                 named_sync(1 + g, 128);
             }
@@ -338,18 +368,30 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_matmul_tc(const __grid_consta
         if (warp < kTcEpiWarps && !s->abort) {
             uint32_t ti, tj;
             tc_tile(a, first, ti, tj);
-            TcColumns<X, O> col;
-            col.set(a.m, (size_t)tj * 256 + half * 128 + lane * 4);
+            TcColumns<X, O, VEC> col;
+            col.set(a.m, (size_t)tj * 256 + half * 128, lane);
             for (uint32_t r = split + S * warp; r < NT; r += S * kTcEpiWarps) {
                 const size_t i = (size_t)ti * NT + r;
                 if (i >= a.m.m || !col.live) break;
-                const uint32_t at = smem_u32(sums + r * 128 + lane * 4);
-                float4 z = ld_cluster_f4(map_rank(at, half));
-                for (uint32_t p = 1; p < S; ++p) {
-                    const float4 w = ld_cluster_f4(map_rank(at, 2 * p + half));
-                    z.x += w.x, z.y += w.y, z.z += w.z, z.w += w.w;
+                typename TcColumns<X, O, VEC>::template Rows<X, 1> res;
+                typename TcColumns<X, O, VEC>::template Rows<O, 1> old;
+                if (a.m.residual) res.load(col, a.m.residual, a.m.ldr, i, a.m.m);
+                if (a.m.accumulate) old.load(col, a.m.out, a.m.ldo, i, a.m.m);
+                float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+                const uint32_t at = smem_u32(sums + r * 128);
+                for (uint32_t p = 0; p < S; ++p) {
+                    const uint32_t from = map_rank(at, 2 * p + half);
+                    const float4 w = VEC ? ld_cluster_f4(from + lane * 16)
+                                         : make_float4(ld_cluster_f(from + lane * 4), ld_cluster_f(from + lane * 4 + 128),
+                                                       ld_cluster_f(from + lane * 4 + 256),
+                                                       ld_cluster_f(from + lane * 4 + 384));
+                    sum.x += w.x, sum.y += w.y, sum.z += w.z, sum.w += w.w;
                 }
-                col.finish(a.m, i, z);
+                float z[4];
+                col.activate(a.m, i, sum, z);
+                if (a.m.residual) res.add(0, col.live, z);
+                if (a.m.accumulate) old.add(0, col.live, z);
+                col.template store<O>(a.m.out, i * a.m.ldo, z);
             }
         }
     }

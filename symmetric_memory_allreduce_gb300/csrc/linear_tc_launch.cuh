@@ -33,9 +33,18 @@ inline bool encode_map(CUtensorMap* map, sym_dtype_t t, const void* p, size_t ro
                                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Whether the epilogue can take four neighbouring columns at a time (TcColumns).
+inline bool columns_in_fours(const MatmulArgs& m, size_t xs, size_t os) {
+    return m.n % 4 == 0 && (uintptr_t)m.out % (4 * os) == 0 && m.ldo % 4 == 0 &&
+           (!m.residual || ((uintptr_t)m.residual % (4 * xs) == 0 && m.ldr % 4 == 0)) &&
+           (!m.pre || ((uintptr_t)m.pre % (4 * xs) == 0 && m.ldp % 4 == 0));
+}
+
 template <class X, class O, bool A_MN, bool B_MN, int NT>
 sym_status_t launch_tc(const MatmulArgs& m, sym_dtype_t t, uint32_t splits, cudaStream_t st) {
-    const void* kernel = (const void*)k_matmul_tc<X, O, A_MN, B_MN, NT>;
+    const bool vec = columns_in_fours(m, sizeof(X), sizeof(O));
+    const void* kernel = vec ? (const void*)k_matmul_tc<X, O, A_MN, B_MN, NT, true>
+                             : (const void*)k_matmul_tc<X, O, A_MN, B_MN, NT, false>;
     int dev = 0;
     SYM_CUDA(cudaGetDevice(&dev));
     DevCtx* ctx = dev_ctx(dev);
@@ -59,10 +68,10 @@ sym_status_t launch_tc(const MatmulArgs& m, sym_dtype_t t, uint32_t splits, cuda
     a.timeout_ns = default_timeout_ns();
     if ((uint64_t)a.tiles_i * a.tiles_j >= (1ull << 26)) return SYM_ERR_UNSUPPORTED;
     const uint32_t tiles = a.tiles_i * a.tiles_j;
-    static std::atomic<uint64_t> ready{0};                // devices whose limit is set
-    if (dev >= 64 || !(ready.load(std::memory_order_acquire) >> dev & 1)) {
+    static std::atomic<uint64_t> ready[2];                // devices whose limit is set
+    if (dev >= 64 || !(ready[vec].load(std::memory_order_acquire) >> dev & 1)) {
         SYM_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kTcSmem));
-        if (dev < 64) ready.fetch_or(1ull << dev, std::memory_order_release);
+        if (dev < 64) ready[vec].fetch_or(1ull << dev, std::memory_order_release);
     }
     const uint32_t pairs = (uint32_t)ctx->num_sms / 2;
     cudaLaunchConfig_t cfg{};

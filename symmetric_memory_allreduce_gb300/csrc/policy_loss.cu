@@ -11,6 +11,7 @@
 // The sums over a row are held in binary32.  A row of weight 0 is not read:
 // its outputs are 0 whatever stands there.
 #include <cmath>
+#include <type_traits>
 
 #include "tensor.cuh"
 #include "training.cuh"
@@ -43,17 +44,28 @@ struct RowTerms {
     bool clipped;
 };
 
-__device__ __forceinline__ RowTerms row_terms(const PolicyArgs& a, size_t t, float logp) {
+// A row's inputs but its logits.
+struct RowInputs {
+    float A, old, ref, go;
+    __device__ __forceinline__ RowInputs(const PolicyArgs& a, size_t t) {
+        A = a.adv[t];
+        old = a.old_logp[t];
+        ref = a.ref_logp ? a.ref_logp[t] : 0.f;
+        go = a.grad_out ? *a.grad_out : 1.f;
+    }
+};
+
+__device__ __forceinline__ RowTerms row_terms(const PolicyArgs& a, const RowInputs& in, float logp) {
     RowTerms o;
-    const float A = a.adv[t];
-    const float d0 = logp - a.old_logp[t], d = fminf(fmaxf(d0, -kClampLog), kClampLog);
+    const float A = in.A;
+    const float d0 = logp - in.old, d = fminf(fmaxf(d0, -kClampLog), kClampLog);
     const float rho = expf(d), bounded = fminf(fmaxf(rho, a.lo), a.hi);
     o.clipped = bounded * A < rho * A;
     o.policy = d0 != d0 ? d0 : -fminf(rho * A, bounded * A);
     o.slope = o.clipped || fabsf(d0) > kClampLog ? 0.f : -A * rho;
     o.kl = 0.f;
     if (a.ref_logp) {
-        const float k0 = a.ref_logp[t] - logp, k = fminf(fmaxf(k0, -kClampLog), kClampLog);
+        const float k0 = in.ref - logp, k = fminf(fmaxf(k0, -kClampLog), kClampLog);
         const float kr = expf(k);
         o.kl = k0 != k0 ? k0 : kr - k - 1.f;
         if (!(fabsf(k0) > kClampLog)) o.slope += a.beta * (1.f - kr);
@@ -98,11 +110,55 @@ __device__ __forceinline__ uint32_t minus_inf_bits<__nv_bfloat16>() { return 0xF
 template <>
 __device__ __forceinline__ uint32_t minus_inf_bits<__half>() { return 0xFC00FC00u; }
 
+// Element pair k of a vector.
 template <class X>
-__device__ __forceinline__ void unpack(const uint4& v, float (&f)[Row<X>::E]) {
-    const X* h = reinterpret_cast<const X*>(&v);
-#pragma unroll
-    for (int e = 0; e < Row<X>::E; ++e) f[e] = to_f(h[e]);
+__device__ __forceinline__ void unpack2(const uint4& v, int k, float& x, float& y) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    if (sizeof(X) == 4) {
+        x = __uint_as_float(w[2 * k]), y = __uint_as_float(w[2 * k + 1]);
+    } else if (std::is_same<X, __nv_bfloat16>::value) {
+        x = __uint_as_float(w[k] << 16), y = __uint_as_float(w[k] & 0xFFFF0000u);
+    } else {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[k]));
+        x = f.x, y = f.y;
+    }
+}
+
+template <class X>
+__device__ __forceinline__ void pack2(uint4& v, int k, float x, float y) {
+    uint32_t* w = &v.x;
+    if (sizeof(X) == 4) {
+        w[2 * k] = __float_as_uint(x), w[2 * k + 1] = __float_as_uint(y);
+    } else if (std::is_same<X, __nv_bfloat16>::value) {
+        const __nv_bfloat162 b = __floats2bfloat162_rn(x, y);
+        w[k] = *reinterpret_cast<const uint32_t*>(&b);
+    } else {
+        const __half2 h = __floats2half2_rn(x, y);
+        w[k] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+}
+
+// Largest of a vector's elements and m; NaN elements are passed over (their exponentials are NaN).
+template <class X>
+__device__ __forceinline__ float max_vector(const uint4& v, float m) {
+    if (sizeof(X) == 4) {
+        m = fmaxf(m, fmaxf(__uint_as_float(v.x), __uint_as_float(v.y)));
+        return fmaxf(m, fmaxf(__uint_as_float(v.z), __uint_as_float(v.w)));
+    }
+    float x, y;
+    uint4 t;
+    if (std::is_same<X, __nv_bfloat16>::value) {
+        const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&v);
+        const __nv_bfloat162 b = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
+        t.x = *reinterpret_cast<const uint32_t*>(&b);
+    } else {
+        const __half2* h = reinterpret_cast<const __half2*>(&v);
+        const __half2 b = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
+        t.x = *reinterpret_cast<const uint32_t*>(&b);
+    }
+    t.y = t.z = t.w = 0;
+    unpack2<X>(t, 0, x, y);
+    return fmaxf(m, fmaxf(x, y));
 }
 
 // Vector v of a row; what lies outside the row's V elements reads as -infinity (weight 0).
@@ -135,26 +191,22 @@ __device__ __forceinline__ void store_vector(const Row<X>& r, int phase, int64_t
         if (j + e >= 0 && j + e < V) r.p[j + e] = h[e];
 }
 
-__device__ __forceinline__ float exp2_approx(float x) {      // 2 ulp; exp2(-inf) = 0
+__device__ __forceinline__ float exp2_approx(float x) {      // 2 ulp; below 2^-126: 0
     float y;
-    asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
 
-// Running maximum m and sum s of exp2(c x - c m) over a vector's elements.
+// Adds exp2(c x - b) of a vector's elements to two sums.
 template <class X>
-__device__ __forceinline__ void add_vector(const uint4& v, float c, float& m, float& s) {
-    constexpr int E = Row<X>::E;
-    float x[E];
-    unpack<X>(v, x);
-    float M = m;
+__device__ __forceinline__ void add_vector(const uint4& v, F2 c, F2 b, F2& s) {
 #pragma unroll
-    for (int e = 0; e < E; ++e) M = fmaxf(M, x[e]);
-    const float b = M == -INFINITY ? 0.f : M * c;            // all -inf so far: every term is 0
-    s *= m == M ? 1.f : exp2_approx(fmaf(m, c, -b));
-#pragma unroll
-    for (int e = 0; e < E; ++e) s += exp2_approx(fmaf(x[e], c, -b));
-    m = M;
+    for (int k = 0; k < Row<X>::E / 2; ++k) {
+        float x, y;
+        unpack2<X>(v, k, x, y);
+        split(fma2(f2(x, y), c, b), x, y);
+        s = add2(s, f2(exp2_approx(x), exp2_approx(y)));
+    }
 }
 
 // Joins two (maximum, sum) pairs.
@@ -184,15 +236,16 @@ __device__ __forceinline__ RowGrad row_grad(float coef, float lse) {
 // Its magnitudes are 2^(c x + shift): one product, one exponential, one rounding an element; the sign
 // is set on the rounded word.
 template <class X>
-__device__ __forceinline__ uint4 grad_vector(const uint4& v, float c, const RowGrad& g) {
-    constexpr int E = Row<X>::E;
-    float x[E];
-    unpack<X>(v, x);
+__device__ __forceinline__ uint4 grad_vector(const uint4& v, F2 c, F2 shift, uint32_t flip) {
     uint4 o;
-    X* h = reinterpret_cast<X*>(&o);
 #pragma unroll
-    for (int e = 0; e < E; ++e) h[e] = from_f<X>(exp2_approx(fmaf(x[e], c, g.shift)));
-    o.x ^= g.flip, o.y ^= g.flip, o.z ^= g.flip, o.w ^= g.flip;
+    for (int k = 0; k < Row<X>::E / 2; ++k) {
+        float x, y;
+        unpack2<X>(v, k, x, y);
+        split(fma2(f2(x, y), c, shift), x, y);
+        pack2<X>(o, k, exp2_approx(x), exp2_approx(y));
+    }
+    o.x ^= flip, o.y ^= flip, o.z ^= flip, o.w ^= flip;
     return o;
 }
 
@@ -227,6 +280,9 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) k_policy_loss(PolicyA
             for (int64_t v = v0; v < v1; v += THREADS) store_vector<X>(d, x.phase, v, V, make_uint4(0, 0, 0, 0));
         return;
     }
+    const RowInputs in(a, t);
+    const int64_t y = a.targets[t];
+    const float xy = to_f(x.p[y]);                           // before a gradient in place can replace it
     if (C > 1) cluster_arrive();                             // waited for before the first remote store
     const float c = a.inv_t * 1.44269504f;
     float m = -INFINITY, s = 0.f;
@@ -235,12 +291,19 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) k_policy_loss(PolicyA
 #pragma unroll
         for (int k = 0; k < VPT; ++k)
             r[k] = v + k * THREADS < v1 ? load_vector<X>(x, v + k * THREADS, V) : make_uint4(inf, inf, inf, inf);
+        float M = m;
 #pragma unroll
-        for (int k = 0; k < VPT; ++k) add_vector<X>(r[k], c, m, s);
+        for (int k = 0; k < VPT; ++k) M = max_vector<X>(r[k], M);
+        const float b = M == -INFINITY ? 0.f : -M * c;       // all -inf so far: every term is 0
+        F2 sum = f2(KEEP ? 0.f : s * exp2_approx(fmaf(m, c, b)), 0.f);
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) add_vector<X>(r[k], f2(c, c), f2(b, b), sum);
+        float s1;
+        split(sum, s, s1);
+        s += s1;
+        m = M;
         if (KEEP) break;
     }
-    const int64_t y = a.targets[t];
-    const float xy = to_f(x.p[y]);                           // before a gradient in place can replace it
     const float wm = warp_max(m);
     s = warp_sum(s * exp2_approx(fmaf(m, c, wm == -INFINITY ? 0.f : -wm * c)));
     if (threadIdx.x % 32 == 0) {
@@ -274,10 +337,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) k_policy_loss(PolicyA
             a.logp[t] = logp;
             a.lse[t] = lse;
         }
-        if (a.dlogits) {
-            const float go = a.grad_out ? *a.grad_out : 1.f;
-            s_g = row_grad<X>(go * w * row_terms(a, t, logp).slope * a.inv_t, lse);
-        }
+        if (a.dlogits) s_g = row_grad<X>(in.go * w * row_terms(a, in, logp).slope * a.inv_t, lse);
     }
     if (!a.dlogits) return;
     __syncthreads();
@@ -288,7 +348,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) k_policy_loss(PolicyA
             const int64_t u = v + k * THREADS;
             if (u >= v1) break;
             if (!KEEP) r[k] = load_vector<X>(x, u, V);
-            store_vector<X>(d, x.phase, u, V, grad_vector<X>(r[k], c, g));
+            store_vector<X>(d, x.phase, u, V, grad_vector<X>(r[k], f2(c, c), f2(g.shift, g.shift), g.flip));
             fix_target<X>(d, x.phase, u, y, c, xy, g);
         }
         if (KEEP) break;
@@ -321,8 +381,8 @@ __global__ void __launch_bounds__(kBackThreads) k_policy_backward(PolicyArgs a, 
     const int64_t y = a.targets[t];
     const float c = a.inv_t * 1.44269504f;
     if (threadIdx.x == 0) {
-        const float go = a.grad_out ? *a.grad_out : 1.f;
-        s_g = row_grad<X>(go * w * row_terms(a, t, a.logp[t]).slope * a.inv_t, a.lse[t]);
+        const RowInputs in(a, t);
+        s_g = row_grad<X>(in.go * w * row_terms(a, in, a.logp[t]).slope * a.inv_t, a.lse[t]);
     }
     __syncthreads();
     const RowGrad g = s_g;
@@ -332,7 +392,7 @@ __global__ void __launch_bounds__(kBackThreads) k_policy_backward(PolicyArgs a, 
         if (v >= vectors) break;
         const bool target = y >= j && y < j + Row<X>::E;
         const float xy = target ? to_f(x.p[y]) : 0.f;        // this thread's own vector: not yet replaced
-        store_vector<X>(d, x.phase, v, V, grad_vector<X>(r[k], c, g));
+        store_vector<X>(d, x.phase, v, V, grad_vector<X>(r[k], f2(c, c), f2(g.shift, g.shift), g.flip));
         if (target) fix_target<X>(d, x.phase, v, y, c, xy, g);
     }
 }
@@ -344,22 +404,22 @@ constexpr int kStatsThreads = 512;
 
 template <int THREADS>
 __global__ void __launch_bounds__(THREADS) k_policy_stats(PolicyArgs a) {
-    __shared__ double red[THREADS / 32];
+    __shared__ float red[THREADS / 32];
     asm volatile("griddepcontrol.wait;" ::: "memory");       // launched while the rows' kernel still runs
-    double s[4] = {0., 0., 0., 0.};
+    float s[4] = {0.f, 0.f, 0.f, 0.f};
     for (size_t t = threadIdx.x; t < a.T; t += THREADS) {
         float w = a.weights ? a.weights[t] : 1.f;
         const int64_t y = a.targets[t];
         if (w == 0.f || y < 0 || (uint64_t)y >= a.V) continue;
-        const RowTerms r = row_terms(a, t, a.logp[t]);
-        s[0] += (double)(w * (r.policy + a.beta * r.kl));
-        s[1] += (double)(w * r.policy);
-        s[2] += (double)(w * r.kl);
-        s[3] += r.clipped ? (double)w : 0.;
+        const RowTerms r = row_terms(a, RowInputs(a, t), a.logp[t]);
+        s[0] += w * (r.policy + a.beta * r.kl);
+        s[1] += w * r.policy;
+        s[2] += w * r.kl;
+        s[3] += r.clipped ? w : 0.f;
     }
     for (int i = 0; i < 4; ++i) {
-        const double v = block_sum<THREADS>(s[i], red);
-        if (threadIdx.x == 0) a.stats[i] = (float)v;
+        const float v = block_sum<THREADS>(s[i], red);
+        if (threadIdx.x == 0) a.stats[i] = v;
     }
 }
 
@@ -380,6 +440,13 @@ static LossShape loss_shape(size_t T, size_t vectors, int num_sms) {
     while (s.cluster < 8 && s.vpt > 2 && T * s.cluster < (size_t)num_sms) s.cluster *= 2, s.vpt /= 2;
     s.keep = (size_t)s.threads * s.vpt * s.cluster >= vectors;
     return s;
+}
+
+// 16-byte vectors that a row can touch: one more where rows start between their boundaries.
+static size_t row_vectors(const void* logits, size_t ld, size_t rows, size_t vocab, size_t es) {
+    const size_t per = 16 / es;
+    const bool aligned = (uintptr_t)logits % 16 == 0 && (rows == 1 || ld % per == 0);
+    return ceil_div(vocab + (aligned ? 0 : per - 1), per);
 }
 
 template <class X>
@@ -462,7 +529,7 @@ sym_status_t sym_policy_loss(const void* logits, size_t ld, size_t rows, size_t 
     cudaStream_t st = (cudaStream_t)stream;
     a.status = ctx->status;
     if (rows) {
-        const size_t per = 16 / dtype_size(dtype), vectors = ceil_div(vocab + per - 1, per);
+        const size_t vectors = row_vectors(logits, ld, rows, vocab, dtype_size(dtype));
         const LossShape sh = loss_shape(rows, vectors, ctx->num_sms);
         if (rows * sh.cluster >= (1ull << 31)) return SYM_ERR_UNSUPPORTED;
         int64_t run = (int64_t)ceil_div(vectors, (size_t)sh.cluster);
@@ -502,8 +569,8 @@ sym_status_t sym_policy_loss_backward(const void* logits, size_t ld, size_t rows
     if (!ctx) return SYM_ERR_CUDA;
     a.status = ctx->status;
     cudaStream_t st = (cudaStream_t)stream;
-    const size_t per = 16 / dtype_size(dtype);
-    const size_t bpr = ceil_div(ceil_div(vocab + per - 1, per), (size_t)(kBackThreads * kBackVectors));
+    const size_t bpr = ceil_div(row_vectors(logits, ld, rows, vocab, dtype_size(dtype)),
+                                (size_t)(kBackThreads * kBackVectors));
     if (rows * bpr >= (1ull << 31)) return SYM_ERR_UNSUPPORTED;
     const unsigned grid = (unsigned)(rows * bpr);
     switch (dtype) {

@@ -32,6 +32,37 @@ __device__ __forceinline__ float load_f(const void* p, size_t i) { return to_f(s
 template <class T>
 __device__ __forceinline__ void store_f(void* p, size_t i, float x) { static_cast<T*>(p)[i] = from_f<T>(x); }
 
+// Two binary32 operations per instruction, each rounded once (no contraction across them).
+struct F2 {
+    uint64_t v;
+};
+__device__ __forceinline__ F2 f2(float x, float y) {
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ void split(F2 a, float& x, float& y) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(a.v));
+}
+// a*b + z with z = (-0, -0) is a*b rounded once, signs of zero included.  z is a kernel argument: a
+// packed product the compiler can see is contracted with the sum that follows it (measured: other
+// bits than mul and add apart).
+__device__ __forceinline__ F2 mul2(F2 a, F2 b, F2 z) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(z.v));
+    return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+
 __device__ __forceinline__ float warp_max(float x) {
 #pragma unroll
     for (int o = 16; o; o >>= 1) x = fmaxf(x, __shfl_xor_sync(~0u, x, o));
