@@ -97,7 +97,7 @@ __global__ void __launch_bounds__(kDzThreads) k_linear_dz(DzArgs a) {
             if (r >= r1) continue;
             if (a.pre) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) d[u][e] *= act_slope(z[u][e], a.act);
+                for (int e = 0; e < 8; ++e) d[u][e] *= act_slope<X>(z[u][e], a.act);
             }
 #pragma unroll
             for (int e = 0; e < 8; ++e) s[e] += d[u][e];
@@ -191,21 +191,23 @@ static Span span(const void* p, size_t rows, size_t n, size_t ld, size_t es) {
 }
 static bool meet(Span x, Span y) { return x.a < y.b && y.a < x.b; }
 
-// Tile rows and k shares of a tensor-core product: the least of an estimate in clocks.  A pair's step of
-// 64 k takes the longer of its four instructions (2 NT clocks) and of its copies (32 + NT/8 KB for the
-// pair at about 64 bytes a clock and SM); a tile's epilogue about 12 clocks a row and runs under the next tile's
-// steps; sharing k out costs a cluster's exchange.
-static void tc_shape(const MatmulArgs& m, bool b_mn, int num_sms, int* nt_out, uint32_t* splits_out) {
+// Tile rows NT and k shares S of a tensor-core product: the least of an estimate in clocks, fitted to
+// measured times of 40 shapes (within 15 % of the fastest choice for all of them).  A step of 64 k
+// takes 210 + NT clocks (its copies) or 2 NT (its four instructions); all of them no less than the
+// operands' bytes take from memory; a tile's epilogue 850 + 18 a row, under the next tile's steps.  With
+// S shares a tile is a cluster of 2S CTAs, of which the GPU holds `held[S]` at once.
+static void tc_shape(const MatmulArgs& m, bool b_mn, const uint32_t* held, int* nt_out, uint32_t* splits_out) {
     const double kblocks = (double)ceil_div(m.kk, (size_t)64), tj = (double)ceil_div(m.n, (size_t)256);
+    const double memory = (double)(m.m + m.n) * (double)m.kk * 2 / 3500;
     double best = 1e300;
     for (int nt = b_mn ? 128 : 16; nt <= 256; nt *= 2) {
-        const double tiles = tj * (double)ceil_div(m.m, (size_t)nt);
+        const double tiles = tj * (double)ceil_div(m.m, (size_t)nt), step = std::max(2.0 * nt, 210.0 + nt);
+        const double epi = 850 + 18 * std::min<double>(nt, (double)m.m);
         for (uint32_t s = 1; s <= 4; s *= 2) {
-            if (s > 1 && (kblocks < 4 * s || nt > 128)) continue;
-            const double step = std::max(2.0 * nt, 256.0 + nt), main = std::ceil(kblocks / s) * step;
-            const double epi = 12.0 * std::min<double>(nt, (double)m.m) / (s > 1 ? s : 1) + (s > 1 ? 2500 : 0);
-            const double waves = std::ceil(tiles * s / (num_sms / 2));
-            const double t = waves * std::max(main, s > 1 ? main + epi : epi) + (s > 1 ? 0 : epi);
+            if (s > 1 && (kblocks < 4 * s || nt > 128 || held[s] == 0)) continue;
+            const double waves = std::ceil(tiles / held[s]), main = std::ceil(kblocks / s) * step;
+            const double t = s == 1 ? std::max(waves * std::max(main, epi), memory) + epi
+                                    : std::max(waves * main, memory) + waves * (epi / s + 2500) + (waves - 1) * 6000;
             if (t < best) best = t, *nt_out = nt, *splits_out = s;
         }
     }
@@ -225,7 +227,9 @@ static sym_status_t matmul(const MatmulArgs& m, sym_dtype_t in, sym_dtype_t out,
     if (!ctx) return SYM_ERR_CUDA;
     int nt = 256;
     uint32_t splits = 1;
-    tc_shape(m, b_mn, ctx->num_sms, &nt, &splits);
+    uint32_t held[5];
+    SYM_TRY(matmul_tc_held(dev, ctx->num_sms, held));
+    tc_shape(m, b_mn, held, &nt, &splits);
     return in == SYM_BF16 ? matmul_tc_bf16(m, out, a_mn, b_mn, nt, splits, st)
                           : matmul_tc_f16(m, out, a_mn, b_mn, nt, splits, st);
 }
@@ -281,7 +285,7 @@ sym_status_t sym_linear(const void* x, size_t ldx, const void* w, size_t ldw, co
     sym_status_t s = align_operand(x, ldx, M, K, dtype, ws, st);
     if (s == SYM_OK) s = align_operand(w, ldw, N, K, dtype, ws, st);
     if (s != SYM_OK) return s;
-    MatmulArgs m{x, w, ldx, 1, ldw, 1, M, N, K, bias, residual, ldr, pre, ldp, y, ldy, (int)act, false};
+    MatmulArgs m{x, w, ldx, 1, ldw, 1, M, N, K, bias, residual, ldr, pre, ldp, y, ldy, (int)act};
     return matmul(m, dtype, dtype, false, false, st);
 }
 
@@ -378,14 +382,14 @@ sym_status_t sym_linear_backward(const void* dy, size_t lddy, const void* x, siz
     }
     if (dx && M && K) {
         // dX(m,k) = sum_n dZ(m,n) W(n,k)
-        MatmulArgs m{dz, w, lddz, 1, 1, ldw, M, K, N, nullptr, nullptr, 0, nullptr, 0, dx, lddx, SYM_ACT_NONE, false};
+        MatmulArgs m{dz, w, lddz, 1, 1, ldw, M, K, N, nullptr, nullptr, 0, nullptr, 0, dx, lddx, SYM_ACT_NONE};
         sym_status_t s = matmul(m, dtype, dtype, true, false, st);
         if (s != SYM_OK) return s;
     }
     if (dw && N && K) {
         // dW(n,k) = sum_m dZ(m,n) X(m,k)
-        MatmulArgs m{dz, x, 1, lddz, 1, ldx, N, K, M, nullptr, nullptr, 0, nullptr, 0, dw, lddw, SYM_ACT_NONE,
-                     accumulate != 0};
+        MatmulArgs m{dz, x, 1, lddz, 1, ldx, N, K, M, nullptr, accumulate ? dw : nullptr, lddw, nullptr, 0, dw, lddw,
+                     SYM_ACT_NONE};
         sym_status_t s = matmul(m, dtype, grad_dtype, true, true, st);
         if (s != SYM_OK) return s;
     }

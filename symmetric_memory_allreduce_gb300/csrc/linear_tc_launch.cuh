@@ -33,16 +33,28 @@ inline bool encode_map(CUtensorMap* map, sym_dtype_t t, const void* p, size_t ro
                                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Whether the epilogue can take four neighbouring columns at a time (TcColumns).
-inline bool columns_in_fours(const MatmulArgs& m, size_t xs, size_t os) {
-    return m.n % 4 == 0 && (uintptr_t)m.out % (4 * os) == 0 && m.ldo % 4 == 0 &&
-           (!m.residual || ((uintptr_t)m.residual % (4 * xs) == 0 && m.ldr % 4 == 0)) &&
-           (!m.pre || ((uintptr_t)m.pre % (4 * xs) == 0 && m.ldp % 4 == 0));
+// Whether the epilogue can take eight neighbouring columns at a time (TcRows).
+inline bool columns_in_eights(const MatmulArgs& m) {
+    return m.n % 8 == 0 && (uintptr_t)m.out % 16 == 0 && m.ldo % 8 == 0 &&
+           (!m.residual || ((uintptr_t)m.residual % 16 == 0 && m.ldr % 8 == 0)) &&
+           (!m.pre || ((uintptr_t)m.pre % 16 == 0 && m.ldp % 8 == 0));
+}
+
+inline void tc_config(cudaLaunchConfig_t& cfg, cudaLaunchAttribute& attr, uint32_t grid, uint32_t splits, cudaStream_t st) {
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(kTcThreads);
+    cfg.dynamicSmemBytes = kTcSmem;
+    cfg.stream = st;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = 2 * splits;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
 }
 
 template <class X, class O, bool A_MN, bool B_MN, int NT>
 sym_status_t launch_tc(const MatmulArgs& m, sym_dtype_t t, uint32_t splits, cudaStream_t st) {
-    const bool vec = columns_in_fours(m, sizeof(X), sizeof(O));
+    const bool vec = columns_in_eights(m);
     const void* kernel = vec ? (const void*)k_matmul_tc<X, O, A_MN, B_MN, NT, true>
                              : (const void*)k_matmul_tc<X, O, A_MN, B_MN, NT, false>;
     int dev = 0;
@@ -63,6 +75,7 @@ sym_status_t launch_tc(const MatmulArgs& m, sym_dtype_t t, uint32_t splits, cuda
     a.tiles_j = (uint32_t)ceil_div(m.n, (size_t)256);
     a.group = 8;
     a.kblocks = (uint32_t)ceil_div(m.kk, (size_t)kTcBK);
+    while (splits > a.kblocks) splits /= 2;               // a pair without terms would have nothing to commit
     a.splits = splits;
     a.status = ctx->status;
     a.timeout_ns = default_timeout_ns();
@@ -75,16 +88,8 @@ sym_status_t launch_tc(const MatmulArgs& m, sym_dtype_t t, uint32_t splits, cuda
     }
     const uint32_t pairs = (uint32_t)ctx->num_sms / 2;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(splits > 1 ? tiles * 2 * splits : 2 * std::min(tiles, pairs));
-    cfg.blockDim = dim3(kTcThreads);
-    cfg.dynamicSmemBytes = kTcSmem;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2 * splits;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cudaLaunchAttribute attr{};
+    tc_config(cfg, attr, splits > 1 ? tiles * 2 * splits : 2 * std::min(tiles, pairs), splits, st);
     void* args[] = {&a};
     SYM_CUDA(cudaLaunchKernelExC(&cfg, kernel, args));
     count_launch();
