@@ -21,7 +21,7 @@ namespace symar {
 // their shared memory, so the bias's gradient needs no scratch and no second
 // launch and is the same bits every time.
 
-constexpr int kDzThreads = 256, kDzCols = 64, kDzCluster = 8, kDzUnroll = 4;
+constexpr int kDzThreads = 256, kDzCols = 64, kDzCluster = 8;
 
 struct DzArgs {
     const void* dy;
@@ -32,25 +32,26 @@ struct DzArgs {
     size_t ldz;
     void* db;              // null: not wanted
     size_t M, N;
-    int act;
     bool accumulate, vec;  // vec: every row of dy, pre and dz starts at a 16-byte boundary
 };
 
+// Eight elements of a row, of which `live` exist, as they are in memory.
 template <class X>
-__device__ __forceinline__ void load_row(const void* p, size_t at, int live, bool vec, float (&f)[8]) {
-    const X* q = static_cast<const X*>(p) + at;
-    if (vec && live == 8) {
-        uint4 v[sizeof(X) / 2];
+struct RowItem {
+    uint4 v[sizeof(X) / 2];
+    __device__ __forceinline__ void load(const void* p, size_t at, int live, bool vec) {
+        const X* q = static_cast<const X*>(p) + at;
+        if (vec && live == 8) {
 #pragma unroll
-        for (int k = 0; k < (int)sizeof(X) / 2; ++k) v[k] = __ldcs(reinterpret_cast<const uint4*>(q) + k);
-        const X* h = reinterpret_cast<const X*>(v);
+            for (int k = 0; k < (int)sizeof(X) / 2; ++k) v[k] = __ldcs(reinterpret_cast<const uint4*>(q) + k);
+        } else {
+            X* h = reinterpret_cast<X*>(v);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] = to_f(h[e]);
-    } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] = e < live ? to_f(q[e]) : 0.f;
+            for (int e = 0; e < 8; ++e) h[e] = e < live ? q[e] : from_f<X>(0.f);
+        }
     }
-}
+    __device__ __forceinline__ float operator[](int e) const { return to_f(reinterpret_cast<const X*>(v)[e]); }
+};
 
 template <class X>
 __device__ __forceinline__ void store_row(void* p, size_t at, int live, bool vec, const float (&f)[8]) {
@@ -69,9 +70,9 @@ __device__ __forceinline__ void store_row(void* p, size_t at, int live, bool vec
     }
 }
 
-template <class X, class O>
-__global__ void __launch_bounds__(kDzThreads) k_linear_dz(DzArgs a) {
-    constexpr int LANES = kDzCols / 8, ROWS = kDzThreads / LANES;
+template <class X, class O, int ACT>
+__global__ void __launch_bounds__(kDzThreads, 3) k_linear_dz(DzArgs a) {
+    constexpr int LANES = kDzCols / 8, ROWS = kDzThreads / LANES, UNROLL = sizeof(X) == 2 ? 4 : 2;
     __shared__ float red[ROWS][kDzCols + 4];
     __shared__ float sums[kDzCluster][kDzCols];              // the first block's: every block's sums
     const uint32_t rank = cluster_rank();
@@ -82,26 +83,27 @@ __global__ void __launch_bounds__(kDzThreads) k_linear_dz(DzArgs a) {
     const size_t r0 = rank * strip, r1 = min(r0 + strip, a.M);
     cluster_arrive();                                        // waited for before the first remote store
     float s[8] = {};
-    for (size_t i = r0 + ty; live && i < r1; i += (size_t)ROWS * kDzUnroll) {
-        float d[kDzUnroll][8], z[kDzUnroll][8];
+    for (size_t i = r0 + ty; live && i < r1; i += (size_t)ROWS * UNROLL) {
+        RowItem<X> dy[UNROLL], z[UNROLL];
 #pragma unroll
-        for (int u = 0; u < kDzUnroll; ++u) {
+        for (int u = 0; u < UNROLL; ++u) {
             const size_t r = i + (size_t)u * ROWS;
             if (r >= r1) continue;
-            load_row<X>(a.dy, r * a.ldy + j, live, a.vec, d[u]);
-            if (a.pre) load_row<X>(a.pre, r * a.ldp + j, live, a.vec, z[u]);
+            dy[u].load(a.dy, r * a.ldy + j, live, a.vec);
+            if (ACT != SYM_ACT_NONE) z[u].load(a.pre, r * a.ldp + j, live, a.vec);
         }
 #pragma unroll
-        for (int u = 0; u < kDzUnroll; ++u) {
+        for (int u = 0; u < UNROLL; ++u) {
             const size_t r = i + (size_t)u * ROWS;
             if (r >= r1) continue;
-            if (a.pre) {
+            float d[8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) d[u][e] *= act_slope<X>(z[u][e], a.act);
+            for (int e = 0; e < 8; ++e) {
+                d[e] = dy[u][e];
+                if (ACT != SYM_ACT_NONE) d[e] *= act_slope<X>(z[u][e], ACT);
+                s[e] += d[e];
             }
-#pragma unroll
-            for (int e = 0; e < 8; ++e) s[e] += d[u][e];
-            if (a.dz) store_row<X>(a.dz, r * a.ldz + j, live, a.vec, d[u]);
+            if (a.dz) store_row<X>(a.dz, r * a.ldz + j, live, a.vec, d);
         }
     }
 #pragma unroll
@@ -122,6 +124,16 @@ __global__ void __launch_bounds__(kDzThreads) k_linear_dz(DzArgs a) {
         for (int r = 0; r < kDzCluster; ++r) t += sums[r][threadIdx.x];
         store_f<O>(a.db, j0 + threadIdx.x, t);
     }
+}
+
+template <class X, class O>
+static const void* dz_kernel(int act) {
+    switch (act) {
+        case SYM_ACT_RELU: return (const void*)k_linear_dz<X, O, SYM_ACT_RELU>;
+        case SYM_ACT_GELU: return (const void*)k_linear_dz<X, O, SYM_ACT_GELU>;
+        case SYM_ACT_SILU: return (const void*)k_linear_dz<X, O, SYM_ACT_SILU>;
+    }
+    return (const void*)k_linear_dz<X, O, SYM_ACT_NONE>;
 }
 
 // ---------------------------------------------------------------- unaligned operands
@@ -339,7 +351,7 @@ sym_status_t sym_linear_backward(const void* dy, size_t lddy, const void* x, siz
     const void* dz = dy;
     size_t lddz = lddy;
     if (N && (act != SYM_ACT_NONE || dbias)) {
-        DzArgs d{dy, lddy, act == SYM_ACT_NONE ? nullptr : pre, ldp, nullptr, 0, dbias, M, N, (int)act,
+        DzArgs d{dy, lddy, act == SYM_ACT_NONE ? nullptr : pre, ldp, nullptr, 0, dbias, M, N,
                  accumulate != 0, false};
         if (act != SYM_ACT_NONE && (dx || dw)) {
             d.dz = ws;
@@ -350,14 +362,11 @@ sym_status_t sym_linear_backward(const void* dy, size_t lddy, const void* x, siz
         const size_t row = 16 / es;
         d.vec = (uintptr_t)dy % 16 == 0 && lddy % row == 0 &&
                 (!d.pre || ((uintptr_t)pre % 16 == 0 && ldp % row == 0));
-        const void* k = nullptr;
-        switch (dtype) {
-            case SYM_F32: k = (const void*)k_linear_dz<float, float>; break;
-            case SYM_BF16: k = grad_dtype == SYM_F32 ? (const void*)k_linear_dz<__nv_bfloat16, float>
-                                                     : (const void*)k_linear_dz<__nv_bfloat16, __nv_bfloat16>; break;
-            case SYM_F16: k = grad_dtype == SYM_F32 ? (const void*)k_linear_dz<__half, float>
-                                                    : (const void*)k_linear_dz<__half, __half>; break;
-        }
+        const void* k = dtype == SYM_F32    ? dz_kernel<float, float>(act)
+                        : dtype == SYM_BF16 ? (grad_dtype == SYM_F32 ? dz_kernel<__nv_bfloat16, float>(act)
+                                                                     : dz_kernel<__nv_bfloat16, __nv_bfloat16>(act))
+                                            : (grad_dtype == SYM_F32 ? dz_kernel<__half, float>(act)
+                                                                     : dz_kernel<__half, __half>(act));
         cudaLaunchConfig_t cfg{};
         cfg.gridDim = dim3((unsigned)(ceil_div(N, (size_t)kDzCols) * kDzCluster));
         cfg.blockDim = dim3(kDzThreads);
