@@ -207,18 +207,21 @@ static bool meet(Span x, Span y) { return x.a < y.b && y.a < x.b; }
 // measured times of 40 shapes (within 15 % of the fastest choice for all of them).  A step of 64 k
 // takes 210 + NT clocks (its copies) or 2 NT (its four instructions); all of them no less than the
 // operands' bytes take from memory; a tile's epilogue 850 + 18 a row, under the next tile's steps.  With
-// S shares a tile is a cluster of 2S CTAs, of which the GPU holds `held[S]` at once.
-static void tc_shape(const MatmulArgs& m, bool b_mn, const uint32_t* held, int* nt_out, uint32_t* splits_out) {
+// S shares a tile is a cluster of 2S CTAs, of which the GPU holds `held[S]` at once.  32-bit operands: 1200
+// clocks to split a step's elements or 12 NT for its 24 instructions, epilogues not overlapped.
+static void tc_shape(const MatmulArgs& m, bool f32, bool f32_out, bool b_mn, const uint32_t* held, int* nt_out, uint32_t* splits_out) {
     const double kblocks = (double)ceil_div(m.kk, (size_t)64), tj = (double)ceil_div(m.n, (size_t)256);
-    const double memory = (double)(m.m + m.n) * (double)m.kk * 2 / 3500;
+    const double memory = (double)(m.m + m.n) * (double)m.kk * (f32 ? 4 : 2) / 3500;
+    const int most = f32_out ? 128 : 256;
     double best = 1e300;
-    for (int nt = b_mn ? 128 : 16; nt <= 256; nt *= 2) {
-        const double tiles = tj * (double)ceil_div(m.m, (size_t)nt), step = std::max(2.0 * nt, 210.0 + nt);
+    for (int nt = b_mn ? 128 : 16; nt <= most; nt *= 2) {
+        const double tiles = tj * (double)ceil_div(m.m, (size_t)nt);
+        const double step = f32 ? std::max(12.0 * nt, 1200.0) : std::max(2.0 * nt, 210.0 + nt);
         const double epi = 850 + 18 * std::min<double>(nt, (double)m.m);
         for (uint32_t s = 1; s <= 4; s *= 2) {
             if (s > 1 && (kblocks < 4 * s || nt > 128 || held[s] == 0)) continue;
             const double waves = std::ceil(tiles / held[s]), main = std::ceil(kblocks / s) * step;
-            const double t = s == 1 ? std::max(waves * std::max(main, epi), memory) + epi
+            const double t = s == 1 ? std::max(waves * (f32 ? main + epi : std::max(main, epi)), memory) + epi
                                     : std::max(waves * main, memory) + waves * (epi / s + 2500) + (waves - 1) * 6000;
             if (t < best) best = t, *nt_out = nt, *splits_out = s;
         }
@@ -228,20 +231,45 @@ static void tc_shape(const MatmulArgs& m, bool b_mn, const uint32_t* held, int* 
 #endif
 }
 
-// out = a b^T on the units of its type.  a_mn, b_mn: which index the operands are contiguous along
-// (matmul_tc_bf16).  Without terms (kk = 0) the FMA kernel writes the epilogue of zero.
+// A product without terms: the epilogue of zero.
+template <class X, class O>
+__global__ void __launch_bounds__(256) k_linear_no_terms(MatmulArgs m) {
+    const size_t e = (size_t)blockIdx.x * 256 + threadIdx.x, i = e / m.n, j = e % m.n;
+    if (i >= m.m) return;
+    float z = m.bias ? load_f<X>(m.bias, j) : 0.f;
+    if (m.pre) store_f<X>(m.pre, i * m.ldp + j, z);
+    z = act_value<X>(z, m.act);
+    if (m.residual) z += load_f<O>(m.residual, i * m.ldr + j);
+    store_f<O>(m.out, i * m.ldo + j, z);
+}
+
+static sym_status_t no_terms(const MatmulArgs& m, sym_dtype_t in, sym_dtype_t out, cudaStream_t st) {
+    const size_t blocks = ceil_div(m.m * m.n, (size_t)256);
+    if (blocks >= (1ull << 31)) return SYM_ERR_UNSUPPORTED;
+    const unsigned g = (unsigned)blocks;
+    if (in == SYM_F32) k_linear_no_terms<float, float><<<g, 256, 0, st>>>(m);
+    else if (in == SYM_BF16 && out == SYM_F32) k_linear_no_terms<__nv_bfloat16, float><<<g, 256, 0, st>>>(m);
+    else if (in == SYM_BF16) k_linear_no_terms<__nv_bfloat16, __nv_bfloat16><<<g, 256, 0, st>>>(m);
+    else if (out == SYM_F32) k_linear_no_terms<__half, float><<<g, 256, 0, st>>>(m);
+    else k_linear_no_terms<__half, __half><<<g, 256, 0, st>>>(m);
+    count_launch();
+    SYM_CUDA(cudaGetLastError());
+    return SYM_OK;
+}
+
+// out = a b^T on the tensor cores.  a_mn, b_mn: which index the operands are contiguous along (matmul_tc_bf16).
 static sym_status_t matmul(const MatmulArgs& m, sym_dtype_t in, sym_dtype_t out, bool a_mn, bool b_mn,
                            cudaStream_t st) {
-    if (in == SYM_F32 || m.kk == 0) return matmul_simt(m, in, out, st);
+    if (m.kk == 0) return no_terms(m, in, out, st);
     int dev = 0;
     SYM_CUDA(cudaGetDevice(&dev));
     DevCtx* ctx = dev_ctx(dev);
     if (!ctx) return SYM_ERR_CUDA;
-    int nt = 256;
-    uint32_t splits = 1;
-    uint32_t held[5];
+    int nt = 128;
+    uint32_t splits = 1, held[5];
     SYM_TRY(matmul_tc_held(dev, ctx->num_sms, held));
-    tc_shape(m, b_mn, held, &nt, &splits);
+    tc_shape(m, in == SYM_F32, out == SYM_F32, b_mn, held, &nt, &splits);
+    if (in == SYM_F32) return matmul_f32(m, a_mn, b_mn, nt, splits, st);
     return in == SYM_BF16 ? matmul_tc_bf16(m, out, a_mn, b_mn, nt, splits, st)
                           : matmul_tc_f16(m, out, a_mn, b_mn, nt, splits, st);
 }

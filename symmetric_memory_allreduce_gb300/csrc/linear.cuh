@@ -85,16 +85,6 @@ __device__ __forceinline__ float act_slope(float z, int act) {
     return 1.f;
 }
 
-// One element's epilogue, from the 32-bit sum.
-template <class X, class O>
-__device__ __forceinline__ void epilogue_one(const MatmulArgs& a, size_t i, size_t j, float z) {
-    if (a.bias) z += load_f<X>(a.bias, j);
-    if (a.pre) store_f<X>(a.pre, i * a.ldp + j, z);
-    z = act_value<X>(z, a.act);
-    if (a.residual) z += load_f<O>(a.residual, i * a.ldr + j);
-    store_f<O>(a.out, i * a.ldo + j, z);
-}
-
 // linear_bf16.cu, linear_f16.cu: 16-bit operands on the tensor cores, rows of both operands 16-byte
 // aligned.  a_mn: b is contiguous along j; b_mn: a is contiguous along i.  nt rows of the output per tile
 // (16, 32, 64, 128, 256; b_mn: 128, 256), k shared out to `splits` (1, 2, 4) CTA pairs.
@@ -102,6 +92,9 @@ sym_status_t matmul_tc_bf16(const MatmulArgs& m, sym_dtype_t out, bool a_mn, boo
                             cudaStream_t st);
 sym_status_t matmul_tc_f16(const MatmulArgs& m, sym_dtype_t out, bool a_mn, bool b_mn, int nt, uint32_t splits,
                            cudaStream_t st);
+
+// linear_f32.cu: 32-bit operands on the tensor cores, any strides; nt 16, 32, 64 or 128 (b_mn: 128).
+sym_status_t matmul_f32(const MatmulArgs& m, bool a_mn, bool b_mn, int nt, uint32_t splits, cudaStream_t st);
 
 // How many clusters of 2, 4 and 8 CTAs of these kernels a device holds at once: held[1], held[2], held[4].
 sym_status_t matmul_tc_held(int device, int num_sms, uint32_t* held);
@@ -111,8 +104,5 @@ sym_status_t matmul_tc_held(int device, int num_sms, uint32_t* held);
         sym_status_t s_ = (call);               \
         if (s_ != SYM_OK) return s_;            \
     } while (0)
-
-// linear_simt.cu: products in 32 bits on the FMA units, any strides
-sym_status_t matmul_simt(const MatmulArgs& a, sym_dtype_t in, sym_dtype_t out, cudaStream_t st);
 
 }  // namespace symar

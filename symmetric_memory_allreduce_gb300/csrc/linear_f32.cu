@@ -1,0 +1,396 @@
+// Matrix product of 32-bit operands on the tensor cores.
+//
+// A binary32 number is the exact sum of three bf16 ones, x = x0 + x1 + x2, each the leading 8 bits of
+// what the ones before leave (truncated, so no part overflows).  Of the nine products of parts the six
+// largest are summed,
+//   x y = x0 y0 + (x0 y1 + x1 y0 + x1 y1 + x0 y2 + x2 y0) + O(2^-23 |x y|),
+// the first into one 32-bit accumulator and the five small ones into another: the tensor cores
+// truncate each sum, and a truncation is relative to the accumulator's size.  After every 256 k both
+// are added to registers, rounded to nearest.  24 matrix instructions of 16 k replace 64 k of FMA work: at
+// NT = 128 1536 clocks for 2^21 products a pair, 5 times the FMA units' rate.
+//
+// The tiles and the roles of a CTA pair are those of the 16-bit kernel, but for the operands'
+// way into shared memory: eight warps read them (any strides), split them, and write the three
+// parts' swizzled tiles; the same warps drain the accumulators.
+//
+// An infinity leaves NaN parts, whose products are NaN where the plain one is not: a sum that is
+// not finite is computed again, by one thread, term by term.
+#include <array>
+#include <map>
+#include <mutex>
+
+#include "linear_tc.cuh"
+
+namespace symar {
+
+constexpr int kF32Threads = 288, kF32Workers = 256;
+constexpr int kF32Chunk = 4;                        // steps of 64 k between additions to registers
+constexpr uint32_t kF32PartA = 128 * 64 * 2;        // bytes of one part of A's tile
+
+__host__ __device__ constexpr uint32_t f32_part_b(int NT) { return (uint32_t)NT / 2 * 64 * 2; }
+__host__ __device__ constexpr uint32_t f32_stage(int NT) { return 3 * (kF32PartA + (f32_part_b(NT) < 1024 ? 1024 : f32_part_b(NT))); }
+__host__ __device__ constexpr int f32_stages(int NT) { return NT == 128 ? 2 : 3; }
+constexpr uint32_t kF32Ring = 184 * 1024;
+constexpr size_t kF32Smem = 1024 + kF32Ring + kTcEpiWarps * kTcStaging + 512;
+
+struct F32Args {
+    MatmulArgs m;
+    uint32_t tiles_i, tiles_j, group, kblocks, splits;
+    bool vec_a, vec_b;          // rows of the operand along j / along i start at 16-byte boundaries
+    uint32_t* status;
+    uint64_t timeout_ns;
+};
+
+// ROWS indices x 64 k of one operand, split among the workers: thread t has PER items of four
+// neighbouring elements, `lines` apart.  MN: neighbouring elements are neighbouring indices, a line a
+// k; else they are neighbouring k, a line an index.
+template <bool MN, int ROWS>
+struct F32Tile {
+    static constexpr int LINE = MN ? ROWS / 4 : 16;                          // items per line
+    static constexpr int LINES = MN ? 64 : ROWS, APART = kF32Workers / LINE; // lines in all, and between a thread's items
+    static constexpr int PER = (LINES + APART - 1) / APART;
+    const float* p;          // the thread's first item of the next step
+    size_t apart;            // elements between its items
+    size_t step;             // elements between steps
+    int line;                // line of its first item
+    int lines;               // MN: unused; else lines of the tile that exist
+    int four;                // MN: elements of an item that exist; else the item's first k
+    float4 x[PER];
+
+    // Element (r, k) of the operand is at base[r*sr + k*sk].
+    __device__ __forceinline__ void start(const float* base, size_t sr, size_t sk, size_t r0, size_t rows, size_t k0) {
+        line = (int)threadIdx.x / LINE;
+        const int at = (int)threadIdx.x % LINE * 4;
+        if (MN) {
+            four = r0 + at < rows ? (int)min((size_t)4, rows - r0 - at) : 0;
+            lines = 0;
+            p = base + r0 + at + (k0 + line) * sk;
+            apart = APART * sk;
+            step = 64 * sk;
+        } else {
+            four = at;
+            lines = r0 < rows ? (int)min((size_t)ROWS, rows - r0) : 0;
+            p = base + (r0 + line) * sr + k0 + at;
+            apart = APART * sr;
+            step = 64;
+        }
+    }
+
+    // The next step's elements; `left`: how many of its 64 k exist.
+    __device__ __forceinline__ void load(int left, bool vec) {
+#pragma unroll
+        for (int u = 0; u < PER; ++u) {
+            const int l = line + u * APART;
+            const int have = MN ? (l < left ? four : 0) : (l < lines ? left - four : 0);
+            const float* q = p + u * apart;
+            x[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (vec && have >= 4) {
+                x[u] = __ldg(reinterpret_cast<const float4*>(q));
+            } else {
+                if (have > 0) x[u].x = q[0];
+                if (have > 1) x[u].y = q[1];
+                if (have > 2) x[u].z = q[2];
+                if (have > 3) x[u].w = q[3];
+            }
+        }
+        p += step;
+    }
+
+    // Into the three parts' tiles, `part` bytes apart: rows of 128 bytes (64 k, or 64 indices), the
+    // 16-byte pieces of each swapped by the row's number modulo 8, as the matrix instructions read them.
+    // What is not finite leaves a NaN among its parts.
+    __device__ __forceinline__ void store(uint8_t* tile, uint32_t part) const {
+        const int at = (int)threadIdx.x % LINE * 4;
+        uint8_t* q;
+        if (MN) q = tile + at / 64 * 8192 + line * 128 + ((at % 64 / 8) ^ (line % 8)) * 16 + at % 8 * 2;
+        else q = tile + line * 128 + ((at / 8) ^ (line % 8)) * 16 + at % 8 * 2;
+#pragma unroll
+        for (int u = 0; u < PER; ++u) {
+            if (LINES % APART != 0 && line + u * APART >= LINES) break;
+            const float v[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+            uint32_t b[3][4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                b[0][e] = __float_as_uint(v[e]);
+                const float r = v[e] - __uint_as_float(b[0][e] & 0xFFFF0000u);
+                b[1][e] = __float_as_uint(r);
+                b[2][e] = __float_as_uint(r - __uint_as_float(b[1][e] & 0xFFFF0000u));
+            }
+            // APART is a multiple of 8, so the swap is the same for all of a thread's lines
+            static_assert(APART % 8 == 0, "lines of a thread agree modulo 8");
+#pragma unroll
+            for (int k = 0; k < 3; ++k)
+                *reinterpret_cast<uint2*>(q + k * part + u * APART * 128) =
+                    make_uint2(__byte_perm(b[k][0], b[k][1], 0x7632), __byte_perm(b[k][2], b[k][3], 0x7632));
+        }
+    }
+};
+
+// A sum term by term, for one that came out not finite.
+__device__ __noinline__ float f32_dot(const MatmulArgs& m, size_t i, size_t j) {
+    const float* a = static_cast<const float*>(m.a) + i * m.ai;
+    const float* b = static_cast<const float*>(m.b) + j * m.bj;
+    float s = 0.f;
+    for (size_t k = 0; k < m.kk; ++k) s = fmaf(a[k * m.ak], b[k * m.bk], s);
+    return s;
+}
+
+template <int W, int U>
+__device__ __forceinline__ void f32_mend(const MatmulArgs& m, size_t i, size_t step, size_t j, float (&z)[U][W]) {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int e = 0; e < W; ++e)
+            if (!(fabsf(z[u][e]) <= 3.402823466e38f) && i + u * step < m.m && j + e < m.n)
+                z[u][e] = f32_dot(m, i + u * step, j + e);
+}
+
+template <bool A_MN, bool B_MN, int NT, bool VEC>
+__global__ void __launch_bounds__(kF32Threads, 1) k_matmul_f32(const __grid_constant__ F32Args a) {
+    constexpr int STAGES = f32_stages(NT), CW = NT < 32 || !VEC ? 16 : 32, CHUNKS = NT / CW;
+    constexpr int GROUPS = CHUNKS > 1 ? 2 : 1, MINE = CHUNKS / GROUPS;   // pieces of CW rows that a warp drains
+    constexpr uint32_t PART_B = f32_part_b(NT) < 1024 ? 1024 : f32_part_b(NT), STAGE = f32_stage(NT);
+    constexpr uint32_t COLUMNS = 4 * NT;
+    static_assert(STAGES * STAGE <= kF32Ring && (uint32_t)NT * 512 <= kF32Ring, "the ring holds the stages, or the sums");
+    static_assert(!B_MN || NT >= 128, "a 128-byte swizzle row holds 64 contiguous elements");
+    extern __shared__ uint8_t raw[];
+    uint8_t* ring = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
+    float* staging = reinterpret_cast<float*>(ring + kF32Ring);
+    TcShared* s = reinterpret_cast<TcShared*>(ring + kF32Ring + kTcEpiWarps * kTcStaging);
+
+    const int warp = __shfl_sync(~0u, (int)threadIdx.x / 32, 0), lane = threadIdx.x % 32;
+    const uint32_t rank = cluster_rank(), half = rank & 1, split = rank >> 1, lead = rank & ~1u;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < STAGES; ++i) {
+            mbar_init(&s->full[i], 16);                              // one lane of each worker warp of the pair
+            mbar_init(&s->empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&s->acc_full[i], 1);
+            mbar_init(&s->acc_empty[i], 2 * 4 * GROUPS);
+        }
+        s->abort = 0;
+        fence_mbar_init();
+    }
+    if (warp == 8) tmem_alloc(&s->tmem, COLUMNS);
+    tc_fence_before();
+    __syncwarp();
+    cluster_sync();
+    tc_fence_after();
+    const uint32_t tmem = s->tmem;
+
+    const uint32_t S = a.splits, tiles = a.tiles_i * a.tiles_j;
+    const uint32_t first = blockIdx.x / (2 * S), step = gridDim.x / (2 * S);
+    const uint32_t k0 = (uint32_t)((uint64_t)a.kblocks * split / S), k1 = (uint32_t)((uint64_t)a.kblocks * (split + 1) / S);
+
+    if (warp == 8) {
+        if (half == 0) {
+            constexpr uint32_t idesc = 1u << 4 | 1u << 7 | 1u << 10 | (A_MN ? 1u << 15 : 0u) | (B_MN ? 1u << 16 : 0u) |
+                                       (uint32_t)(NT / 8) << 17 | (256u / 16) << 24;
+            const uint16_t mask = (uint16_t)(3u << lead);
+            const uint64_t da0 = smem_desc(smem_u32(ring), A_MN ? 8192 : 16, 1024);
+            const uint64_t db0 = smem_desc(smem_u32(ring) + 3 * kF32PartA, B_MN ? 8192 : 16, 1024);
+            uint32_t st = 0, ph = 0, n = 0;
+            bool ok = true;
+            for (uint32_t t = first; ok && t < tiles; t += step) {
+                for (uint32_t k = k0; ok && k < k1; ++k) {
+                    const bool start = (k - k0) % kF32Chunk == 0, end = k + 1 == k1 || (k + 1 - k0) % kF32Chunk == 0;
+                    const uint32_t buf = n & 1, acc = tmem + buf * 2 * NT;
+                    if (start) {
+                        if (!(ok = tc_wait_warp(&s->acc_empty[buf], (n >> 1 & 1) ^ 1, a, s, 2))) break;
+                        tc_fence_after();
+                    }
+                    if (!(ok = tc_wait_warp(&s->full[st], ph, a, s, 3))) break;
+                    tc_fence_after();
+                    if (elect_lane()) {
+                        const uint64_t da = da0 + st * (STAGE >> 4), db = db0 + st * (STAGE >> 4);
+#pragma unroll
+                        for (int c = 0; c < 6; ++c) {
+                            constexpr int PA[6] = {0, 0, 1, 1, 0, 2}, PB[6] = {0, 1, 0, 1, 2, 0};
+#pragma unroll
+                            for (int q = 0; q < 4; ++q)
+                                mma_f16_pair(acc + (c ? NT : 0), da + PA[c] * (kF32PartA >> 4) + q * (A_MN ? 128 : 2),
+                                             db + PB[c] * (PART_B >> 4) + q * (B_MN ? 128 : 2), idesc,
+                                             !start || q != 0 || c > 1);
+                        }
+                        mma_commit_pair(&s->empty[st], mask);
+                        if (end) mma_commit_pair(&s->acc_full[buf], mask);
+                    }
+                    __syncwarp();
+                    if (++st == STAGES) st = 0, ph ^= 1;
+                    if (end) ++n;
+                }
+            }
+        }
+    } else {
+        const int g = warp / 4, q = warp % 4;
+        float* stage = staging + warp * (kTcStaging / 4);
+        const uint32_t full0 = map_rank(smem_u32(&s->full[0]), lead), free0 = map_rank(smem_u32(&s->acc_empty[0]), lead);
+        uint32_t st = 0, ph = 1, n = 0;
+        bool ok = true;
+        for (uint32_t t = first; ok && t < tiles; t += step) {
+            uint32_t ti, tj;
+            tc_tile(a, t, ti, tj);
+            const size_t ja = (size_t)tj * 256 + half * 128, ib = (size_t)ti * NT + half * (NT / 2);
+            F32Tile<A_MN, 128> xa;
+            F32Tile<B_MN, NT / 2> xb;
+            xa.start((const float*)a.m.b, a.m.bj, a.m.bk, ja, a.m.n, (size_t)k0 * 64);
+            xb.start((const float*)a.m.a, a.m.ai, a.m.ak, ib, a.m.m, (size_t)k0 * 64);
+            auto load = [&](uint32_t k) {
+                const int left = (int)min((size_t)64, a.m.kk - (size_t)k * 64);
+                xa.load(left, a.vec_a);
+                xb.load(left, a.vec_b);
+            };
+            float sum[MINE][CW];
+#pragma unroll
+            for (int c = 0; c < MINE; ++c)
+#pragma unroll
+                for (int e = 0; e < CW; ++e) sum[c][e] = 0.f;
+            // adds the next finished pair of accumulators to `sum`
+            auto drain = [&]() {
+                const uint32_t buf = n & 1;
+                if (g < GROUPS) {
+                    if (!tc_wait_warp(&s->acc_full[buf], n >> 1 & 1, a, s, 4)) return false;
+                    tc_fence_after();
+#pragma unroll
+                    for (int c = 0; c < MINE; ++c) {
+                        float v[CW];
+                        const uint32_t at = tmem + buf * 2 * NT + (g + c * GROUPS) * CW + ((uint32_t)(q * 32) << 16);
+                        tmem_load(at + NT, v);
+#pragma unroll
+                        for (int e = 0; e < CW; ++e) sum[c][e] += v[e];
+                        tmem_load(at, v);
+#pragma unroll
+                        for (int e = 0; e < CW; ++e) sum[c][e] += v[e];
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_cluster_relaxed(free0 + buf * 8);
+                }
+                ++n;
+                return true;
+            };
+            load(k0);
+            for (uint32_t k = k0; k < k1; ++k) {
+                if (!(ok = tc_wait_warp(&s->empty[st], ph, a, s, 1))) break;
+                uint8_t* tile = ring + st * STAGE;
+                xa.store(tile, kF32PartA);
+                xb.store(tile + 3 * kF32PartA, PART_B);
+                if (k + 1 < k1) load(k + 1);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(full0 + st * 8);
+                if (++st == STAGES) st = 0, ph ^= 1;
+                // the accumulators of the last 256 k are drained when those of the next are under way
+                if ((k + 1 - k0) % kF32Chunk == 0 && k + 1 - k0 > kF32Chunk && !(ok = drain())) break;
+            }
+            const uint32_t chunks = (k1 - k0 + kF32Chunk - 1) / kF32Chunk;
+            const uint32_t drained = (k1 - k0) / kF32Chunk > 0 ? (k1 - k0) / kF32Chunk - 1 : 0;
+            for (uint32_t c = drained; ok && c < chunks; ++c) ok = drain();
+            if (!ok) break;
+            if (S == 1) {
+                constexpr int W = VEC ? 8 : 1, U = VEC ? CW / 8 : CW;
+                constexpr size_t STEP = VEC ? 8 : 1;
+                const size_t j0 = (size_t)tj * 256 + half * 128 + q * 32;
+                const size_t j = VEC ? j0 + lane % 4 * 8 : j0 + lane;
+                float bias[W];
+                load_bias<float>(a.m, j, bias);
+                if (g < GROUPS)
+#pragma unroll
+                    for (int c = 0; c < MINE; ++c) {
+                        const size_t i = (size_t)ti * NT + (g + c * GROUPS) * CW + (VEC ? lane / 4 : 0);
+                        TcRows<float, float, W, U> rows;
+                        rows.read(a.m, i, STEP, j);
+                        float z[U][W];
+                        turn<W, U, CW, VEC>(stage, lane, sum[c], z);
+                        f32_mend(a.m, i, STEP, j, z);
+                        rows.write(a.m, i, STEP, j, bias, z);
+                    }
+            } else {
+                // every worker's stores into the ring came before the products that acc_full tells the end of
+                float* sums = reinterpret_cast<float*>(ring);
+                if (g < GROUPS)
+#pragma unroll
+                    for (int c = 0; c < MINE; ++c)
+#pragma unroll
+                        for (int e = 0; e < CW; ++e) sums[((g + c * GROUPS) * CW + e) * 128 + q * 32 + lane] = sum[c][e];
+            }
+        }
+        if (!ok) s->abort = 1;
+    }
+    if (S > 1) {
+        __syncwarp();
+        cluster_sync();
+        if (warp < kTcEpiWarps && !s->abort) {
+            uint32_t ti, tj;
+            tc_tile(a, first, ti, tj);
+            join_splits<float, float, NT, VEC>(a.m, reinterpret_cast<float*>(ring), ti, tj, half, split, S, warp, lane,
+                                               [&](size_t i, size_t j, auto& z) { f32_mend(a.m, i, 1, j, z); });
+        }
+    }
+    __syncwarp();
+    if (s->abort && lane == 0 && warp == 8) tc_settle();
+    tc_fence_before();
+    __syncwarp();
+    cluster_sync();
+    tc_fence_after();
+    if (warp == 8) tmem_free(tmem, COLUMNS);
+}
+
+template <bool A_MN, bool B_MN, int NT>
+static const void* f32_kernel(bool vec) {
+    return vec ? (const void*)k_matmul_f32<A_MN, B_MN, NT, true> : (const void*)k_matmul_f32<A_MN, B_MN, NT, false>;
+}
+
+static const void* f32_kernel(bool a_mn, bool b_mn, int nt, bool vec) {
+    if (b_mn) return f32_kernel<true, true, 128>(vec);
+    switch (nt) {
+        case 16: return a_mn ? f32_kernel<true, false, 16>(vec) : f32_kernel<false, false, 16>(vec);
+        case 32: return a_mn ? f32_kernel<true, false, 32>(vec) : f32_kernel<false, false, 32>(vec);
+        case 64: return a_mn ? f32_kernel<true, false, 64>(vec) : f32_kernel<false, false, 64>(vec);
+    }
+    return a_mn ? f32_kernel<true, false, 128>(vec) : f32_kernel<false, false, 128>(vec);
+}
+
+static bool fours_aligned(const void* p, size_t ld) { return (uintptr_t)p % 16 == 0 && ld % 4 == 0; }
+
+sym_status_t matmul_f32(const MatmulArgs& m, bool a_mn, bool b_mn, int nt, uint32_t splits, cudaStream_t st) {
+    int dev = 0;
+    SYM_CUDA(cudaGetDevice(&dev));
+    DevCtx* ctx = dev_ctx(dev);
+    if (!ctx) return SYM_ERR_CUDA;
+    F32Args a{};
+    a.m = m;
+    a.tiles_i = (uint32_t)ceil_div(m.m, (size_t)nt);
+    a.tiles_j = (uint32_t)ceil_div(m.n, (size_t)256);
+    a.group = 8;
+    a.kblocks = (uint32_t)ceil_div(m.kk, (size_t)64);
+    while (splits > a.kblocks) splits /= 2;
+    a.splits = splits;
+    a.vec_a = fours_aligned(m.b, a_mn ? m.bk : m.bj);
+    a.vec_b = fours_aligned(m.a, b_mn ? m.ak : m.ai);
+    a.status = ctx->status;
+    a.timeout_ns = default_timeout_ns();
+    if ((uint64_t)a.tiles_i * a.tiles_j >= (1ull << 26)) return SYM_ERR_UNSUPPORTED;
+    const uint32_t tiles = a.tiles_i * a.tiles_j, pairs = (uint32_t)ctx->num_sms / 2;
+    const void* k = f32_kernel(a_mn, b_mn, nt, columns_in_eights(m));
+    {
+        static std::mutex mu;
+        static std::map<std::pair<int, const void*>, bool> ready;
+        std::lock_guard<std::mutex> lk(mu);
+        bool& r = ready[{dev, k}];
+        if (!r) SYM_CUDA(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kF32Smem));
+        r = true;
+    }
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute attr{};
+    tc_config(cfg, attr, splits > 1 ? tiles * 2 * splits : 2 * std::min(tiles, pairs), splits, st);
+    cfg.blockDim = dim3(kF32Threads);
+    cfg.dynamicSmemBytes = kF32Smem;
+    void* args[] = {&a};
+    SYM_CUDA(cudaLaunchKernelExC(&cfg, k, args));
+    count_launch();
+    return SYM_OK;
+}
+
+}  // namespace symar

@@ -30,6 +30,9 @@ namespace symar {
 constexpr int kTcThreads = 320, kTcEpiWarps = 8;
 constexpr int kTcBK = 64;                          // k elements per stage: one 128-byte swizzle row
 constexpr uint32_t kTcStageA = 128 * kTcBK * 2;    // bytes of A per stage and CTA
+// The tensor cores truncate each sum: after n sums a 32-bit accumulator is about n 2^-27.5 too small.
+// Outputs of 32 bits get accumulators of at most 4 steps (16 sums), added up rounded to nearest.
+constexpr uint32_t kTcChunk = 4;
 constexpr uint32_t kTcRing = 192 * 1024;           // bytes of all stages
 constexpr uint32_t kTcStaging = 32 * 32 * 4;       // an epilogue warp's piece
 
@@ -56,7 +59,8 @@ struct TcShared {              // after the ring and the staging
 };
 
 // Waits for a barrier's phase, at most timeout_ns or until another wait of the CTA gave up.
-__device__ __forceinline__ bool tc_wait(uint64_t* bar, uint32_t parity, const TcArgs& a, TcShared* s, uint32_t what) {
+template <class A>
+__device__ __forceinline__ bool tc_wait(uint64_t* bar, uint32_t parity, const A& a, TcShared* s, uint32_t what) {
     if (mbar_try_wait(bar, parity)) return true;
     const uint64_t t0 = globaltimer_ns();
     for (uint32_t it = 1; it < (1u << 30); ++it) {
@@ -71,14 +75,16 @@ __device__ __forceinline__ bool tc_wait(uint64_t* bar, uint32_t parity, const Tc
 }
 
 // The same for a whole warp, whose lanes all get the same answer and stay together.
-__device__ __forceinline__ bool tc_wait_warp(uint64_t* bar, uint32_t parity, const TcArgs& a, TcShared* s, uint32_t what) {
+template <class A>
+__device__ __forceinline__ bool tc_wait_warp(uint64_t* bar, uint32_t parity, const A& a, TcShared* s, uint32_t what) {
     if (__all_sync(~0u, mbar_try_wait(bar, parity))) return true;
     return __all_sync(~0u, tc_wait(bar, parity, a, s, what));
 }
 
 // Tile t of the launch: groups of `group` row tiles, column tiles outer within a group, so the
 // tiles in flight share rows and columns in L2.
-__device__ __forceinline__ void tc_tile(const TcArgs& a, uint32_t t, uint32_t& ti, uint32_t& tj) {
+template <class A>
+__device__ __forceinline__ void tc_tile(const A& a, uint32_t t, uint32_t& ti, uint32_t& tj) {
     const uint32_t per = a.group * a.tiles_j, g = t / per, r = t - g * per;
     const uint32_t gi = min(a.group, a.tiles_i - g * a.group);
     tj = r / gi;
@@ -188,13 +194,87 @@ __device__ __forceinline__ void load_bias(const MatmulArgs& m, size_t j, float (
     for (int e = 0; e < W; ++e) bias[e] = m.bias && j + e < m.n ? load_f<X>(m.bias, j + e) : 0.f;
 }
 
+// A warp's 32 columns (one a lane) x CW rows into the shape that TcRows finishes.  VEC: turned through the
+// warp's 32 x CW words of shared memory, where odd rows swap neighbouring quads so that neither side
+// conflicts: lane l gets columns 8 (l % 4) and on of rows l / 4, l / 4 + 8, ...  Else a copy.
+template <int W, int U, int CW, bool VEC>
+__device__ __forceinline__ void turn(float* stage, int lane, const float (&v)[CW], float (&z)[U][W]) {
+    if (VEC) {
+#pragma unroll
+        for (int r = 0; r < CW; ++r) stage[r * 32 + (lane ^ (r & 1) * 4)] = v[r];
+        __syncwarp();
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int r = lane / 4 + u * 8, quad = lane % 4 * 2;
+            const float4 x = *reinterpret_cast<const float4*>(stage + r * 32 + (quad ^ (r & 1)) * 4);
+            const float4 y = *reinterpret_cast<const float4*>(stage + r * 32 + ((quad + 1) ^ (r & 1)) * 4);
+            z[u][0] = x.x, z[u][1 % W] = x.y, z[u][2 % W] = x.z, z[u][3 % W] = x.w;
+            z[u][4 % W] = y.x, z[u][5 % W] = y.y, z[u][6 % W] = y.z, z[u][7 % W] = y.w;
+        }
+        __syncwarp();
+    } else {
+#pragma unroll
+        for (int u = 0; u < U; ++u) z[u][0] = v[u % CW];
+    }
+}
+
+// The rows split, split + S, ... of a tile whose S sums [NT][128] lie in the cluster's shared memories: adds
+// them in order and finishes them; half a warp on a row of 128 columns, or a warp with single ones.
+template <class X, class O, int NT, bool VEC, class Mend>
+__device__ __forceinline__ void join_splits(const MatmulArgs& m, const float* sums, uint32_t ti, uint32_t tj,
+                                            uint32_t half, uint32_t split, uint32_t S, int warp, int lane, Mend mend) {
+    constexpr int W = VEC ? 8 : 1, C = VEC ? 1 : 4;
+    const uint32_t sub = VEC ? lane / 16 : 0, per = VEC ? 2 : 1;
+    float bias[C][W];
+    size_t j[C];
+#pragma unroll
+    for (int e = 0; e < C; ++e) {
+        j[e] = (size_t)tj * 256 + half * 128 + (VEC ? lane % 16 * 8 : lane + e * 32);
+        load_bias<X>(m, j[e], bias[e]);
+    }
+    for (uint32_t r = split + S * (warp * per + sub); r < NT; r += S * kTcEpiWarps * per) {
+        const size_t i = (size_t)ti * NT + r;
+        if (i >= m.m) break;
+        TcRows<X, O, W, 1> rows[C];
+        float z[C][1][W] = {};
+#pragma unroll
+        for (int e = 0; e < C; ++e) rows[e].read(m, i, 1, j[e]);
+        const uint32_t at = smem_u32(sums + r * 128);
+        for (uint32_t p = 0; p < S; ++p) {
+            const uint32_t from = map_rank(at, 2 * p + half);
+            if (VEC) {
+                const float4 x = ld_cluster_f4(from + lane % 16 * 32), y = ld_cluster_f4(from + lane % 16 * 32 + 16);
+                z[0][0][0] += x.x, z[0][0][1 % W] += x.y, z[0][0][2 % W] += x.z, z[0][0][3 % W] += x.w;
+                z[0][0][4 % W] += y.x, z[0][0][5 % W] += y.y, z[0][0][6 % W] += y.z, z[0][0][7 % W] += y.w;
+            } else {
+#pragma unroll
+                for (int e = 0; e < C; ++e) z[e][0][0] += ld_cluster_f(from + lane * 4 + e * 128);
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < C; ++e) {
+            mend(i, j[e], z[e]);
+            rows[e].write(m, i, 1, j[e], bias[e], z[e]);
+        }
+    }
+}
+
+// After a wait that gave up: copies and products may still be under way; lets them land before the
+// memory is given up.
+__device__ __forceinline__ void tc_settle() {
+    const uint64_t t0 = globaltimer_ns();
+    for (int it = 0; it < 100000 && globaltimer_ns() - t0 < 5000000; ++it) __nanosleep(200);
+}
+
 // A_MN / B_MN: the operand's contiguous index is j / i (else k).
 template <class X, class O, bool A_MN, bool B_MN, int NT, bool VEC>
 __global__ void __launch_bounds__(kTcThreads, 1) k_matmul_tc(const __grid_constant__ TcArgs a) {
     constexpr int STAGES = tc_stages(NT), CW = NT < 32 || !VEC ? 16 : 32, CHUNKS = NT / CW;   // epilogue pieces of CW rows
-    constexpr int GROUPS = CHUNKS > 1 ? 2 : 1;                       // epilogue groups of 4 warps at work
+    constexpr int GROUPS = CHUNKS > 1 ? 2 : 1, MINE = CHUNKS / GROUPS;   // epilogue groups of 4 warps, pieces of a warp
+    constexpr bool LONG = std::is_same<O, float>::value;             // 32-bit outputs: sums of 256 k at most
     constexpr uint32_t STAGE = tc_stage_bytes(NT), COLUMNS = 2 * NT < 32 ? 32 : 2 * NT;
     static_assert(!B_MN || NT >= 128, "a 128-byte swizzle row holds 64 contiguous elements");
+    static_assert(!LONG || NT <= 128, "a thread's sums are in registers");
     extern __shared__ uint8_t raw[];
     uint8_t* ring = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
     float* staging = reinterpret_cast<float*>(ring + kTcRing);
@@ -276,11 +356,15 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_matmul_tc(const __grid_consta
             const uint64_t db0 = smem_desc(smem_u32(ring) + kTcStageA, B_MN ? 8192 : 16, 1024);
             uint32_t st = 0, ph = 0, n = 0;
             bool ok = true;
-            for (uint32_t t = first; ok && t < tiles; t += step, ++n) {
-                const uint32_t buf = n & 1, aph = (n >> 1 & 1) ^ 1, acc = tmem + buf * NT;
-                if (!(ok = tc_wait_warp(&s->acc_empty[buf], aph, a, s, 2))) break;
-                tc_fence_after();
+            for (uint32_t t = first; ok && t < tiles; t += step) {
                 for (uint32_t k = k0; k < k1; ++k) {
+                    const bool start = k == k0 || (LONG && (k - k0) % kTcChunk == 0);
+                    const bool end = k + 1 == k1 || (LONG && (k + 1 - k0) % kTcChunk == 0);
+                    const uint32_t buf = n & 1, acc = tmem + buf * NT;
+                    if (start) {
+                        if (!(ok = tc_wait_warp(&s->acc_empty[buf], (n >> 1 & 1) ^ 1, a, s, 2))) break;
+                        tc_fence_after();
+                    }
                     if (!(ok = tc_wait_warp(&s->full[st], ph, a, s, 3))) break;
                     tc_fence_after();
                     if (elect_lane()) {
@@ -288,135 +372,129 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_matmul_tc(const __grid_consta
 #pragma unroll
                         for (int q = 0; q < kTcBK / 16; ++q)         // 16 k: 32 bytes of a row, or two atoms of 8 rows
                             mma_f16_pair(acc, da + q * (A_MN ? 128 : 2), db + q * (B_MN ? 128 : 2), idesc,
-                                         k != k0 || q != 0);
+                                         !start || q != 0);
                         mma_commit_pair(&s->empty[st], mask);
-                        if (k + 1 == k1) mma_commit_pair(&s->acc_full[buf], mask);
+                        if (end) mma_commit_pair(&s->acc_full[buf], mask);
                     }
                     __syncwarp();
                     if (++st == STAGES) st = 0, ph ^= 1;
+                    if (end) ++n;
                 }
             }
         }
-    } else if (S == 1) {
-        // ---- epilogue: pieces of CW rows i x 128 columns j
+    } else {
+        // ---- epilogue: pieces of CW rows i x 32 columns j a warp, straight from the accumulator or, LONG, from
+        // registers to which the accumulators of each 256 k have been added
         const int g = warp / 4, q = warp % 4;
         float* stage = staging + warp * (kTcStaging / 4);
         constexpr int W = VEC ? 8 : 1, U = VEC ? CW / 8 : CW;
+        constexpr size_t STEP = VEC ? 8 : 1;
+        const uint32_t free0 = map_rank(smem_u32(&s->acc_empty[0]), lead);
+        const uint32_t chunks = LONG ? (k1 - k0 + kTcChunk - 1) / kTcChunk : 1;
         uint32_t n = 0;
-        for (uint32_t t = first; g < GROUPS && t < tiles; t += step, ++n) {
+        bool ok = true;
+        for (uint32_t t = first; ok && g < GROUPS && t < tiles; t += step) {
             uint32_t ti, tj;
             tc_tile(a, t, ti, tj);
-            const uint32_t buf = n & 1;
-            if (!tc_wait_warp(&s->acc_full[buf], n >> 1 & 1, a, s, 4)) break;
-            tc_fence_after();
             const size_t j0 = (size_t)tj * 256 + half * 128 + q * 32;
             const size_t j = VEC ? j0 + lane % 4 * 8 : j0 + lane;
             float bias[W];
             load_bias<X>(a.m, j, bias);
-#pragma unroll 1
-            for (int c = g; c < CHUNKS; c += GROUPS) {
-                // VEC: lane l finishes columns 8 (l % 4) and on of rows l / 4, l / 4 + 8, ...; else column l of all
-                const size_t i = (size_t)ti * NT + c * CW + (VEC ? lane / 4 : 0);
-                constexpr size_t STEP = VEC ? 8 : 1;
-                TcRows<X, O, W, U> rows;
-                rows.read(a.m, i, STEP, j);
-                float v[CW];
-                tmem_load(tmem + buf * NT + c * CW + ((uint32_t)(q * 32) << 16), v);
-                if (c + GROUPS >= CHUNKS) {
+            float sum[LONG ? MINE : 1][CW];
+            if (LONG) {
+#pragma unroll
+                for (int c = 0; c < MINE; ++c)
+#pragma unroll
+                    for (int e = 0; e < CW; ++e) sum[LONG ? c : 0][e] = 0.f;
+                for (uint32_t h = 0; h < chunks; ++h, ++n) {
+                    const uint32_t buf = n & 1;
+                    if (!(ok = tc_wait_warp(&s->acc_full[buf], n >> 1 & 1, a, s, 4))) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int c = 0; c < MINE; ++c) {
+                        float v[CW];
+                        tmem_load(tmem + buf * NT + (g + c * GROUPS) * CW + ((uint32_t)(q * 32) << 16), v);
+#pragma unroll
+                        for (int e = 0; e < CW; ++e) sum[LONG ? c : 0][e] += v[e];
+                    }
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive_cluster_relaxed(map_rank(smem_u32(&s->acc_empty[buf]), lead));
+                    if (lane == 0) mbar_arrive_cluster_relaxed(free0 + buf * 8);
                 }
-                float z[U][W];
-                if (VEC) {
-                    // turned through 32 x CW words; odd rows swap neighbouring quads, so neither side conflicts
-#pragma unroll
-                    for (int r = 0; r < CW; ++r) stage[r * 32 + (lane ^ (r & 1) * 4)] = v[r];
-                    __syncwarp();
-#pragma unroll
-                    for (int u = 0; u < U; ++u) {
-                        const int r = lane / 4 + u * 8, quad = lane % 4 * 2;
-                        const float4 x = *reinterpret_cast<const float4*>(stage + r * 32 + (quad ^ (r & 1)) * 4);
-                        const float4 y = *reinterpret_cast<const float4*>(stage + r * 32 + ((quad + 1) ^ (r & 1)) * 4);
-                        z[u][0] = x.x, z[u][1 % W] = x.y, z[u][2 % W] = x.z, z[u][3 % W] = x.w;
-                        z[u][4 % W] = y.x, z[u][5 % W] = y.y, z[u][6 % W] = y.z, z[u][7 % W] = y.w;
-                    }
-                    __syncwarp();
-                } else {
-#pragma unroll
-                    for (int u = 0; u < U; ++u) z[u][0] = v[u % CW];
-                }
-                rows.write(a.m, i, STEP, j, bias, z);
+            } else {
+                ok = tc_wait_warp(&s->acc_full[n & 1], n >> 1 & 1, a, s, 4);
+                tc_fence_after();
             }
+            if (!ok) break;
+            const uint32_t buf = n & 1;
+#pragma unroll(LONG ? MINE : 1)
+            for (int c = 0; c < MINE; ++c) {
+                const int piece = g + c * GROUPS;
+                const size_t i = (size_t)ti * NT + piece * CW + (VEC ? lane / 4 : 0);
+                TcRows<X, O, W, U> rows;
+                if (S == 1) rows.read(a.m, i, STEP, j);
+                float v[CW];
+                if (LONG) {
+#pragma unroll
+                    for (int e = 0; e < CW; ++e) v[e] = sum[LONG ? c : 0][e];
+                } else {
+                    tmem_load(tmem + buf * NT + piece * CW + ((uint32_t)(q * 32) << 16), v);
+                    if (c + 1 == MINE && S == 1) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive_cluster_relaxed(free0 + buf * 8);
+                    }
+                }
+                if (S == 1) {
+                    float z[U][W];
+                    turn<W, U, CW, VEC>(stage, lane, v, z);
+                    rows.write(a.m, i, STEP, j, bias, z);
+                } else {
+                    // one tile per cluster: the pair's sums into the ring, which is idle by now
+#pragma unroll
+                    for (int r = 0; r < CW; ++r)
+                        reinterpret_cast<float*>(ring)[(piece * CW + r) * 128 + q * 32 + lane] = v[r];
+                }
+            }
+            if (!LONG) ++n;
         }
     }
     if (S > 1) {
-        // ---- one tile per cluster: each pair's sums into shared memory, then every CTA adds its share of rows
-        float* sums = reinterpret_cast<float*>(ring);                // [NT][128]; the ring is idle by now
-        bool ok = true;
-        if (warp < kTcEpiWarps) {
-            ok = tc_wait_warp(&s->acc_full[0], 0, a, s, 4);
-            tc_fence_after();
-            const int g = warp / 4, q = warp % 4;
-            if (ok && g < GROUPS)
-#pragma unroll 1
-                for (int c = g; c < CHUNKS; c += GROUPS) {
-                    float v[CW];
-                    tmem_load(tmem + c * CW + ((uint32_t)(q * 32) << 16), v);
-#pragma unroll
-                    for (int r = 0; r < CW; ++r) sums[(c * CW + r) * 128 + q * 32 + lane] = v[r];
-                }
-        }
         __syncwarp();
         cluster_sync();
         if (warp < kTcEpiWarps && !s->abort) {
             uint32_t ti, tj;
             tc_tile(a, first, ti, tj);
-            // rows split, split + S, ...: half a warp on a row of 128 columns, or a warp with single ones
-            constexpr int W = VEC ? 8 : 1, C = VEC ? 1 : 4;
-            const uint32_t sub = VEC ? lane / 16 : 0, per = VEC ? 2 : 1;
-            float bias[C][W];
-            size_t j[C];
-#pragma unroll
-            for (int e = 0; e < C; ++e) {
-                j[e] = (size_t)tj * 256 + half * 128 + (VEC ? lane % 16 * 8 : lane + e * 32);
-                load_bias<X>(a.m, j[e], bias[e]);
-            }
-            for (uint32_t r = split + S * (warp * per + sub); r < NT; r += S * kTcEpiWarps * per) {
-                const size_t i = (size_t)ti * NT + r;
-                if (i >= a.m.m) break;
-                TcRows<X, O, W, 1> rows[C];
-                float z[C][1][W] = {};
-#pragma unroll
-                for (int e = 0; e < C; ++e) rows[e].read(a.m, i, 1, j[e]);
-                const uint32_t at = smem_u32(sums + r * 128);
-                for (uint32_t p = 0; p < S; ++p) {
-                    const uint32_t from = map_rank(at, 2 * p + half);
-                    if (VEC) {
-                        const float4 x = ld_cluster_f4(from + lane % 16 * 32), y = ld_cluster_f4(from + lane % 16 * 32 + 16);
-                        z[0][0][0] += x.x, z[0][0][1 % W] += x.y, z[0][0][2 % W] += x.z, z[0][0][3 % W] += x.w;
-                        z[0][0][4 % W] += y.x, z[0][0][5 % W] += y.y, z[0][0][6 % W] += y.z, z[0][0][7 % W] += y.w;
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < C; ++e) z[e][0][0] += ld_cluster_f(from + lane * 4 + e * 128);
-                    }
-                }
-#pragma unroll
-                for (int e = 0; e < C; ++e) rows[e].write(a.m, i, 1, j[e], bias[e], z[e]);
-            }
+            join_splits<X, O, NT, VEC>(a.m, reinterpret_cast<float*>(ring), ti, tj, half, split, S, warp, lane,
+                                       [](size_t, size_t, auto&) {});
         }
     }
     __syncwarp();
-    if (s->abort && lane == 0 && warp >= 8) {
-        // copies and products may still be under way: let them land before the memory is given up
-        const uint64_t t0 = globaltimer_ns();
-        for (int it = 0; it < 100000 && globaltimer_ns() - t0 < 5000000; ++it) __nanosleep(200);
-    }
+    if (s->abort && lane == 0 && warp >= 8) tc_settle();
     tc_fence_before();
     __syncwarp();
     cluster_sync();                                                  // no arrival is under way to a CTA that has left
     tc_fence_after();
     if (warp == 9) tmem_free(tmem, COLUMNS);
+}
+
+// Whether the epilogue can take eight neighbouring columns at a time (TcRows).
+inline bool columns_in_eights(const MatmulArgs& m) {
+    return m.n % 8 == 0 && (uintptr_t)m.out % 16 == 0 && m.ldo % 8 == 0 &&
+           (!m.residual || ((uintptr_t)m.residual % 16 == 0 && m.ldr % 8 == 0)) &&
+           (!m.pre || ((uintptr_t)m.pre % 16 == 0 && m.ldp % 8 == 0));
+}
+
+inline void tc_config(cudaLaunchConfig_t& cfg, cudaLaunchAttribute& attr, uint32_t grid, uint32_t splits, cudaStream_t st) {
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(kTcThreads);
+    cfg.dynamicSmemBytes = kTcSmem;
+    cfg.stream = st;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = 2 * splits;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
 }
 
 }  // namespace symar

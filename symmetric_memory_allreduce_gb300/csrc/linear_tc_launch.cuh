@@ -33,25 +33,6 @@ inline bool encode_map(CUtensorMap* map, sym_dtype_t t, const void* p, size_t ro
                                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Whether the epilogue can take eight neighbouring columns at a time (TcRows).
-inline bool columns_in_eights(const MatmulArgs& m) {
-    return m.n % 8 == 0 && (uintptr_t)m.out % 16 == 0 && m.ldo % 8 == 0 &&
-           (!m.residual || ((uintptr_t)m.residual % 16 == 0 && m.ldr % 8 == 0)) &&
-           (!m.pre || ((uintptr_t)m.pre % 16 == 0 && m.ldp % 8 == 0));
-}
-
-inline void tc_config(cudaLaunchConfig_t& cfg, cudaLaunchAttribute& attr, uint32_t grid, uint32_t splits, cudaStream_t st) {
-    cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(kTcThreads);
-    cfg.dynamicSmemBytes = kTcSmem;
-    cfg.stream = st;
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = 2 * splits;
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-}
-
 template <class X, class O, bool A_MN, bool B_MN, int NT>
 sym_status_t launch_tc(const MatmulArgs& m, sym_dtype_t t, uint32_t splits, cudaStream_t st) {
     const bool vec = columns_in_eights(m);
@@ -114,8 +95,8 @@ sym_status_t launch_tc_rows(const MatmulArgs& m, sym_dtype_t t, TcShape s, cudaS
 
 template <class X, class O>
 sym_status_t launch_tc_cols(const MatmulArgs& m, sym_dtype_t t, TcShape s, cudaStream_t st) {
-    if (s.nt == 128) return launch_tc<X, O, true, true, 128>(m, t, s.splits, st);
-    return launch_tc<X, O, true, true, 256>(m, t, s.splits, st);
+    if (s.nt == 128 || sizeof(O) == 4) return launch_tc<X, O, true, true, 128>(m, t, s.splits, st);
+    return launch_tc<X, O, true, true, sizeof(O) == 4 ? 128 : 256>(m, t, s.splits, st);
 }
 
 // The layouts of the three products: forward (both operands contiguous along k), dX (m.b contiguous

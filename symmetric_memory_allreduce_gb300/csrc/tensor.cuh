@@ -57,6 +57,11 @@ __device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
     asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 
+// Arrival at a barrier of the cluster, after this thread's accesses.
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+}
+
 // Arrival at a barrier of the cluster that orders no memory accesses: for tensor memory already read
 // (tcgen05.fence orders that).  A releasing arrival would wait for the thread's global stores first.
 __device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t addr) {
