@@ -10,8 +10,9 @@
 // NT = 128 1536 clocks for 2^21 products a pair, 5 times the FMA units' rate.
 //
 // The tiles and the roles of a CTA pair are those of the 16-bit kernel, but for the operands'
-// way into shared memory: eight warps read them (any strides), split them, and write the three
-// parts' swizzled tiles; the same warps drain the accumulators.
+// way into shared memory: sixteen warps read them (any strides), split them, and write the three
+// parts' swizzled tiles, each thread reading its next step's element as soon as it has written this
+// one's; the same warps drain the accumulators.
 //
 // An infinity leaves NaN parts, whose products are NaN where the plain one is not: a sum that is
 // not finite is computed again, by one thread, term by term.
@@ -23,7 +24,7 @@
 
 namespace symar {
 
-constexpr int kF32Threads = 288, kF32Workers = 256;
+constexpr int kF32Warps = 16, kF32Workers = 32 * kF32Warps, kF32Threads = kF32Workers + 32;
 constexpr int kF32Chunk = 4;                        // steps of 64 k between additions to registers
 constexpr uint32_t kF32PartA = 128 * 64 * 2;        // bytes of one part of A's tile
 
@@ -31,7 +32,8 @@ __host__ __device__ constexpr uint32_t f32_part_b(int NT) { return (uint32_t)NT 
 __host__ __device__ constexpr uint32_t f32_stage(int NT) { return 3 * (kF32PartA + (f32_part_b(NT) < 1024 ? 1024 : f32_part_b(NT))); }
 __host__ __device__ constexpr int f32_stages(int NT) { return NT == 128 ? 2 : 3; }
 constexpr uint32_t kF32Ring = 184 * 1024;
-constexpr size_t kF32Smem = 1024 + kF32Ring + kTcEpiWarps * kTcStaging + 512;
+constexpr uint32_t kF32Staging = 32 * 16 * 4;       // a worker warp's piece of 16 rows
+constexpr size_t kF32Smem = 1024 + kF32Ring + kF32Warps * kF32Staging + 512;
 
 struct F32Args {
     MatmulArgs m;
@@ -76,30 +78,32 @@ struct F32Tile {
         }
     }
 
-    // The next step's elements; `left`: how many of its 64 k exist.
+    // Item u of the next step; `left`: how many of its 64 k exist.
+    __device__ __forceinline__ void load(int u, int left, bool vec) {
+        const int l = line + u * APART;
+        const int have = MN ? (l < left ? four : 0) : (l < lines ? left - four : 0);
+        const float* q = p + u * apart;
+        x[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (vec && have >= 4) {
+            x[u] = __ldg(reinterpret_cast<const float4*>(q));
+        } else {
+            if (have > 0) x[u].x = q[0];
+            if (have > 1) x[u].y = q[1];
+            if (have > 2) x[u].z = q[2];
+            if (have > 3) x[u].w = q[3];
+        }
+    }
+
     __device__ __forceinline__ void load(int left, bool vec) {
 #pragma unroll
-        for (int u = 0; u < PER; ++u) {
-            const int l = line + u * APART;
-            const int have = MN ? (l < left ? four : 0) : (l < lines ? left - four : 0);
-            const float* q = p + u * apart;
-            x[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (vec && have >= 4) {
-                x[u] = __ldg(reinterpret_cast<const float4*>(q));
-            } else {
-                if (have > 0) x[u].x = q[0];
-                if (have > 1) x[u].y = q[1];
-                if (have > 2) x[u].z = q[2];
-                if (have > 3) x[u].w = q[3];
-            }
-        }
+        for (int u = 0; u < PER; ++u) load(u, left, vec);
         p += step;
     }
 
-    // Into the three parts' tiles, `part` bytes apart: rows of 128 bytes (64 k, or 64 indices), the
-    // 16-byte pieces of each swapped by the row's number modulo 8, as the matrix instructions read them.
-    // What is not finite leaves a NaN among its parts.
-    __device__ __forceinline__ void store(uint8_t* tile, uint32_t part) const {
+    // The items into the three parts' tiles, `part` bytes apart, and the next step's items in their place:
+    // rows of 128 bytes (64 k, or 64 indices), the 16-byte pieces of each swapped by the row's number
+    // modulo 8, as the matrix instructions read them.  What is not finite leaves a NaN among its parts.
+    __device__ __forceinline__ void turn_over(uint8_t* tile, uint32_t part, int left, bool vec) {
         const int at = (int)threadIdx.x % LINE * 4;
         uint8_t* q;
         if (MN) q = tile + at / 64 * 8192 + line * 128 + ((at % 64 / 8) ^ (line % 8)) * 16 + at % 8 * 2;
@@ -108,6 +112,7 @@ struct F32Tile {
         for (int u = 0; u < PER; ++u) {
             if (LINES % APART != 0 && line + u * APART >= LINES) break;
             const float v[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+            if (left > 0) load(u, left, vec);
             uint32_t b[3][4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -123,6 +128,7 @@ struct F32Tile {
                 *reinterpret_cast<uint2*>(q + k * part + u * APART * 128) =
                     make_uint2(__byte_perm(b[k][0], b[k][1], 0x7632), __byte_perm(b[k][2], b[k][3], 0x7632));
         }
+        p += step;
     }
 };
 
@@ -147,8 +153,8 @@ __device__ __forceinline__ void f32_mend(const MatmulArgs& m, size_t i, size_t s
 
 template <bool A_MN, bool B_MN, int NT, bool VEC>
 __global__ void __launch_bounds__(kF32Threads, 1) k_matmul_f32(const __grid_constant__ F32Args a) {
-    constexpr int STAGES = f32_stages(NT), CW = NT < 32 || !VEC ? 16 : 32, CHUNKS = NT / CW;
-    constexpr int GROUPS = CHUNKS > 1 ? 2 : 1, MINE = CHUNKS / GROUPS;   // pieces of CW rows that a warp drains
+    constexpr int STAGES = f32_stages(NT), CW = 16, CHUNKS = NT / CW;
+    constexpr int GROUPS = CHUNKS < 4 ? CHUNKS : 4, MINE = CHUNKS / GROUPS;   // pieces of CW rows that a warp drains
     constexpr uint32_t PART_B = f32_part_b(NT) < 1024 ? 1024 : f32_part_b(NT), STAGE = f32_stage(NT);
     constexpr uint32_t COLUMNS = 4 * NT;
     static_assert(STAGES * STAGE <= kF32Ring && (uint32_t)NT * 512 <= kF32Ring, "the ring holds the stages, or the sums");
@@ -156,13 +162,14 @@ __global__ void __launch_bounds__(kF32Threads, 1) k_matmul_f32(const __grid_cons
     extern __shared__ uint8_t raw[];
     uint8_t* ring = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
     float* staging = reinterpret_cast<float*>(ring + kF32Ring);
-    TcShared* s = reinterpret_cast<TcShared*>(ring + kF32Ring + kTcEpiWarps * kTcStaging);
+    TcShared* s = reinterpret_cast<TcShared*>(ring + kF32Ring + kF32Warps * kF32Staging);
 
     const int warp = __shfl_sync(~0u, (int)threadIdx.x / 32, 0), lane = threadIdx.x % 32;
     const uint32_t rank = cluster_rank(), half = rank & 1, split = rank >> 1, lead = rank & ~1u;
     if (threadIdx.x == 0) {
         for (int i = 0; i < STAGES; ++i) {
-            mbar_init(&s->full[i], 16);                              // one lane of each worker warp of the pair
+            mbar_init(&s->full[i], kF32Warps);                       // one lane of each of the CTA's worker warps
+            mbar_init(&s->full[4 + i], 1);                           // in the first CTA: the second's are in too
             mbar_init(&s->empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -172,7 +179,7 @@ __global__ void __launch_bounds__(kF32Threads, 1) k_matmul_f32(const __grid_cons
         s->abort = 0;
         fence_mbar_init();
     }
-    if (warp == 8) tmem_alloc(&s->tmem, COLUMNS);
+    if (warp == kF32Warps) tmem_alloc(&s->tmem, COLUMNS);
     tc_fence_before();
     __syncwarp();
     cluster_sync();
@@ -183,7 +190,7 @@ __global__ void __launch_bounds__(kF32Threads, 1) k_matmul_f32(const __grid_cons
     const uint32_t first = blockIdx.x / (2 * S), step = gridDim.x / (2 * S);
     const uint32_t k0 = (uint32_t)((uint64_t)a.kblocks * split / S), k1 = (uint32_t)((uint64_t)a.kblocks * (split + 1) / S);
 
-    if (warp == 8) {
+    if (warp == kF32Warps) {
         if (half == 0) {
             constexpr uint32_t idesc = 1u << 4 | 1u << 7 | 1u << 10 | (A_MN ? 1u << 15 : 0u) | (B_MN ? 1u << 16 : 0u) |
                                        (uint32_t)(NT / 8) << 17 | (256u / 16) << 24;
@@ -201,6 +208,7 @@ __global__ void __launch_bounds__(kF32Threads, 1) k_matmul_f32(const __grid_cons
                         tc_fence_after();
                     }
                     if (!(ok = tc_wait_warp(&s->full[st], ph, a, s, 3))) break;
+                    if (!(ok = tc_wait_warp(&s->full[4 + st], ph, a, s, 3))) break;
                     tc_fence_after();
                     if (elect_lane()) {
                         const uint64_t da = da0 + st * (STAGE >> 4), db = db0 + st * (STAGE >> 4);
@@ -221,11 +229,24 @@ __global__ void __launch_bounds__(kF32Threads, 1) k_matmul_f32(const __grid_cons
                     if (end) ++n;
                 }
             }
+        } else {
+            // the second CTA's: tells the first that its own tiles are in.  The workers' arrivals stay in
+            // their CTA, since one that is released to the cluster waits for the reads in flight.
+            const uint32_t there = map_rank(smem_u32(&s->full[4]), lead);
+            uint32_t st = 0, ph = 0;
+            bool ok = true;
+            for (uint32_t t = first; ok && t < tiles; t += step)
+                for (uint32_t k = k0; k < k1; ++k) {
+                    if (!(ok = tc_wait_warp(&s->full[st], ph, a, s, 3))) break;
+                    if (elect_lane()) mbar_arrive_cluster(there + st * 8);
+                    __syncwarp();
+                    if (++st == STAGES) st = 0, ph ^= 1;
+                }
         }
     } else {
         const int g = warp / 4, q = warp % 4;
-        float* stage = staging + warp * (kTcStaging / 4);
-        const uint32_t full0 = map_rank(smem_u32(&s->full[0]), lead), free0 = map_rank(smem_u32(&s->acc_empty[0]), lead);
+        float* stage = staging + warp * (kF32Staging / 4);
+        const uint32_t free0 = map_rank(smem_u32(&s->acc_empty[0]), lead);
         uint32_t st = 0, ph = 1, n = 0;
         bool ok = true;
         for (uint32_t t = first; ok && t < tiles; t += step) {
@@ -236,11 +257,9 @@ __global__ void __launch_bounds__(kF32Threads, 1) k_matmul_f32(const __grid_cons
             F32Tile<B_MN, NT / 2> xb;
             xa.start((const float*)a.m.b, a.m.bj, a.m.bk, ja, a.m.n, (size_t)k0 * 64);
             xb.start((const float*)a.m.a, a.m.ai, a.m.ak, ib, a.m.m, (size_t)k0 * 64);
-            auto load = [&](uint32_t k) {
-                const int left = (int)min((size_t)64, a.m.kk - (size_t)k * 64);
-                xa.load(left, a.vec_a);
-                xb.load(left, a.vec_b);
-            };
+            auto left = [&](uint32_t k) { return k < k1 ? (int)min((size_t)64, a.m.kk - (size_t)k * 64) : 0; };
+            xa.load(left(k0), a.vec_a);
+            xb.load(left(k0), a.vec_b);
             float sum[MINE][CW];
 #pragma unroll
             for (int c = 0; c < MINE; ++c)
@@ -270,16 +289,14 @@ __global__ void __launch_bounds__(kF32Threads, 1) k_matmul_f32(const __grid_cons
                 ++n;
                 return true;
             };
-            load(k0);
             for (uint32_t k = k0; k < k1; ++k) {
                 if (!(ok = tc_wait_warp(&s->empty[st], ph, a, s, 1))) break;
                 uint8_t* tile = ring + st * STAGE;
-                xa.store(tile, kF32PartA);
-                xb.store(tile + 3 * kF32PartA, PART_B);
-                if (k + 1 < k1) load(k + 1);
+                xa.turn_over(tile, kF32PartA, left(k + 1), a.vec_a);
+                xb.turn_over(tile + 3 * kF32PartA, PART_B, left(k + 1), a.vec_b);
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(full0 + st * 8);
+                if (lane == 0) mbar_arrive(&s->full[st]);
                 if (++st == STAGES) st = 0, ph ^= 1;
                 // the accumulators of the last 256 k are drained when those of the next are under way
                 if ((k + 1 - k0) % kF32Chunk == 0 && k + 1 - k0 > kF32Chunk && !(ok = drain())) break;
@@ -329,12 +346,12 @@ __global__ void __launch_bounds__(kF32Threads, 1) k_matmul_f32(const __grid_cons
         }
     }
     __syncwarp();
-    if (s->abort && lane == 0 && warp == 8) tc_settle();
+    if (s->abort && lane == 0 && warp == kF32Warps) tc_settle();
     tc_fence_before();
     __syncwarp();
     cluster_sync();
     tc_fence_after();
-    if (warp == 8) tmem_free(tmem, COLUMNS);
+    if (warp == kF32Warps) tmem_free(tmem, COLUMNS);
 }
 
 template <bool A_MN, bool B_MN, int NT>
