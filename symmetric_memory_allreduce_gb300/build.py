@@ -21,7 +21,7 @@ ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
               "--fmad=false", "-Xptxas", "-v", "-I", INCLUDE]
 SOURCES = ["window.cu", "allreduce.cu", "allreduce_f32.cu", "allreduce_bf16.cu", "allreduce_f16.cu",
-           "fused.cu", "p2p.cu", "noalloc.cu", "linear.cu", "linear_f32.cu", "linear_bf16.cu", "linear_f16.cu",
+           "fused.cu", "p2p.cu", "noalloc.cu", "linear.cu", "linear_f32.cu", "linear_skinny.cu", "linear_bf16.cu", "linear_f16.cu",
            "policy_loss.cu", "adamw.cu"]
 
 

@@ -257,14 +257,15 @@ static sym_status_t no_terms(const MatmulArgs& m, sym_dtype_t in, sym_dtype_t ou
     return SYM_OK;
 }
 
-// out = a b^T on the tensor cores.  a_mn, b_mn: which index the operands are contiguous along (matmul_tc_bf16).
-static sym_status_t matmul(const MatmulArgs& m, sym_dtype_t in, sym_dtype_t out, bool a_mn, bool b_mn,
-                           cudaStream_t st) {
+static sym_status_t matmul(const MatmulArgs& m, sym_dtype_t in, sym_dtype_t out, Product product, cudaStream_t st) {
     if (m.kk == 0) return no_terms(m, in, out, st);
     int dev = 0;
     SYM_CUDA(cudaGetDevice(&dev));
     DevCtx* ctx = dev_ctx(dev);
     if (!ctx) return SYM_ERR_CUDA;
+    if (matmul_is_skinny(product == Product::kDw ? m.kk : m.m, in, product))
+        return matmul_skinny(m, in, out, product, ctx->num_sms, st);
+    const bool a_mn = product != Product::kForward, b_mn = product == Product::kDw;
     int nt = 128;
     uint32_t splits = 1, held[5];
     SYM_TRY(matmul_tc_held(dev, ctx->num_sms, held));
@@ -326,13 +327,14 @@ sym_status_t sym_linear(const void* x, size_t ldx, const void* w, size_t ldw, co
     if (s == SYM_OK) s = align_operand(w, ldw, N, K, dtype, ws, st);
     if (s != SYM_OK) return s;
     MatmulArgs m{x, w, ldx, 1, ldw, 1, M, N, K, bias, residual, ldr, pre, ldp, y, ldy, (int)act};
-    return matmul(m, dtype, dtype, false, false, st);
+    return matmul(m, dtype, dtype, Product::kForward, st);
 }
 
 size_t sym_linear_backward_workspace(const void* dy, size_t lddy, const void* x, size_t ldx, const void* w, size_t ldw,
                                      size_t M, size_t N, size_t K, sym_dtype_t dtype, sym_act_t act) {
     return dz_bytes(M, N, dtype_size(dtype), act) +
-           (act == SYM_ACT_NONE ? align_bytes(dy, M, N, lddy, dtype) : 0) + align_bytes(x, M, K, ldx, dtype) +
+           (act == SYM_ACT_NONE ? align_bytes(dy, M, N, lddy, dtype) : 0) +
+           (matmul_is_skinny(M, dtype, Product::kDw) ? 0 : align_bytes(x, M, K, ldx, dtype)) +
            align_bytes(w, N, K, ldw, dtype);
 }
 
@@ -412,22 +414,23 @@ sym_status_t sym_linear_backward(const void* dy, size_t lddy, const void* x, siz
     char* at = ws + dz_bytes(M, N, es, act);
     if ((dx && M && K) || (dw && N && K)) {
         sym_status_t s = SYM_OK;
-        if (N && M && dz == dy) s = align_operand(dz, lddz, M, N, dtype, at, st);
-        if (s == SYM_OK && dw && N && M) s = align_operand(x, ldx, M, K, dtype, at, st);
+        const bool skinny = matmul_is_skinny(M, dtype, Product::kDw);
+        if (N && M && dz == dy && (dx || !skinny)) s = align_operand(dz, lddz, M, N, dtype, at, st);
+        if (s == SYM_OK && dw && N && M && !skinny) s = align_operand(x, ldx, M, K, dtype, at, st);
         if (s == SYM_OK && dx && N && M) s = align_operand(w, ldw, N, K, dtype, at, st);
         if (s != SYM_OK) return s;
     }
     if (dx && M && K) {
         // dX(m,k) = sum_n dZ(m,n) W(n,k)
         MatmulArgs m{dz, w, lddz, 1, 1, ldw, M, K, N, nullptr, nullptr, 0, nullptr, 0, dx, lddx, SYM_ACT_NONE};
-        sym_status_t s = matmul(m, dtype, dtype, true, false, st);
+        sym_status_t s = matmul(m, dtype, dtype, Product::kDx, st);
         if (s != SYM_OK) return s;
     }
     if (dw && N && K) {
         // dW(n,k) = sum_m dZ(m,n) X(m,k)
         MatmulArgs m{dz, x, 1, lddz, 1, ldx, N, K, M, nullptr, accumulate ? dw : nullptr, lddw, nullptr, 0, dw, lddw,
                      SYM_ACT_NONE};
-        sym_status_t s = matmul(m, dtype, grad_dtype, true, true, st);
+        sym_status_t s = matmul(m, dtype, grad_dtype, Product::kDw, st);
         if (s != SYM_OK) return s;
     }
     return SYM_OK;

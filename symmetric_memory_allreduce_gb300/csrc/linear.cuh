@@ -96,6 +96,15 @@ sym_status_t matmul_tc_f16(const MatmulArgs& m, sym_dtype_t out, bool a_mn, bool
 // linear_f32.cu: 32-bit operands on the tensor cores, any strides; nt 16, 32, 64 or 128 (b_mn: 128).
 sym_status_t matmul_f32(const MatmulArgs& m, bool a_mn, bool b_mn, int nt, uint32_t splits, cudaStream_t st);
 
+// The three products and their layouts: forward (both operands contiguous along k), dX (m.b contiguous
+// along j), dW (m.b along j, m.a along i).
+enum class Product { kForward, kDx, kDw };
+
+// linear_skinny.cu: few rows (m.m; kDw: few terms, m.kk), any strides.
+bool matmul_is_skinny(size_t rows, sym_dtype_t in, Product product);
+sym_status_t matmul_skinny(const MatmulArgs& m, sym_dtype_t in, sym_dtype_t out, Product product, int num_sms,
+                           cudaStream_t st);
+
 // How many clusters of 2, 4 and 8 CTAs of these kernels a device holds at once: held[1], held[2], held[4].
 sym_status_t matmul_tc_held(int device, int num_sms, uint32_t* held);
 

@@ -1,0 +1,295 @@
+// The linear layer's products for a few rows (tokens being generated, tiny batches), on the FMA units.
+//
+// With so few rows a product is a pass over the weights: it cannot do without reading W once (forward,
+// dX) or writing dW once.  Here each weight is read by one thread, 16 bytes at a time, multiplied with the
+// rows' elements and summed in 32 bits; the partial sums of a long axis are joined in a fixed order.
+//
+// Where this beats the tensor-core kernels (measured, 4096 x 4096 and 16384 x 4096, us; here / there):
+//   32-bit forward  1 row 13.7 / 40, 4 rows 21 / 40, 8 rows 116 / 74 (the larger)    up to 4 rows
+//   32-bit dX       1 row 21 / 39, 2 rows 23 / 39, 4 rows 44 / 39                    up to 2 rows
+//   dW, 32 bits     1 row 72 / 187, 8 rows 147 / 187 (the larger)                    up to 8 rows
+//   dW, 16 bits     1 row 22 / 43 (the larger), 4 rows 13 / 15, 8 rows 36 / 15       up to 4 rows
+//   16-bit forward and dX: 1 row 28 / 24 and 72 / 24 (the larger)                    never
+#include "linear_tc.cuh"
+
+namespace symar {
+
+constexpr int kSkThreads = 256, kSkWarps = 8;
+
+// V elements at p + q, zeros from `end` on.
+template <int V, bool VEC>
+__device__ __forceinline__ void sk_load(const float* p, size_t q, size_t end, float (&f)[V]) {
+    if (VEC && q + V <= end) {
+        const float4 v = __ldcs(reinterpret_cast<const float4*>(p + q));
+        f[0] = v.x, f[1 % V] = v.y, f[2 % V] = v.z, f[3 % V] = v.w;
+    } else {
+#pragma unroll
+        for (int e = 0; e < V; ++e) f[e] = q + e < end ? p[q + e] : 0.f;
+    }
+}
+
+// ---------------------------------------------------------------- out(i,j) = sum_k x(i,k) w(j,k)
+//
+// A group of `wk` warps takes two columns j and shares their k; a lane has 16 bytes of four steps of both
+// columns' weights on their way.  VEC = false: rows not aligned, an element a lane.
+template <int MT, bool VEC>
+__global__ void __launch_bounds__(kSkThreads) k_skinny_forward(MatmulArgs m, int wk) {
+    constexpr int V = VEC ? 4 : 1, J = 2, AHEAD = 4;
+    __shared__ float part[kSkWarps][J * MT];
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, group = warp / wk, share = warp % wk;
+    const size_t j0 = ((size_t)blockIdx.x * (kSkWarps / wk) + group) * J;
+    const float* x = static_cast<const float*>(m.a);
+    const size_t stride = (size_t)wk * 32 * V;
+    float s[J][MT] = {};
+    if (j0 < m.n) {
+        const float* w0 = static_cast<const float*>(m.b) + j0 * m.bj;
+        const float* w1 = static_cast<const float*>(m.b) + min(j0 + 1, m.n - 1) * m.bj;
+        for (size_t k = (size_t)(share * 32 + lane) * V; k < m.kk; k += stride * AHEAD) {
+            float f[AHEAD][J][V];
+            if (VEC && k + stride * (AHEAD - 1) + V <= m.kk) {   // all inside: the reads leave together
+#pragma unroll
+                for (int u = 0; u < AHEAD; ++u) {
+                    sk_load<V, VEC>(w0, k + u * stride, ~(size_t)0, f[u][0]);
+                    sk_load<V, VEC>(w1, k + u * stride, ~(size_t)0, f[u][1]);
+                }
+            } else {
+#pragma unroll
+                for (int u = 0; u < AHEAD; ++u) {
+                    sk_load<V, VEC>(w0, k + u * stride, m.kk, f[u][0]);
+                    sk_load<V, VEC>(w1, k + u * stride, m.kk, f[u][1]);
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < AHEAD; ++u)
+#pragma unroll
+                for (int i = 0; i < MT; ++i) {
+                    if ((size_t)i >= m.m) break;
+                    float g[V];
+                    sk_load<V, VEC>(x + i * m.ai, k + u * stride, m.kk, g);
+#pragma unroll
+                    for (int e = 0; e < V; ++e) {
+                        s[0][i] = fmaf(g[e], f[u][0][e], s[0][i]);
+                        s[1][i] = fmaf(g[e], f[u][1][e], s[1][i]);
+                    }
+                }
+        }
+    }
+#pragma unroll
+    for (int c = 0; c < J; ++c)
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+            const float t = warp_sum(s[c][i]);
+            if (lane == 0) part[warp][c * MT + i] = t;
+        }
+    __syncthreads();
+    if (share == 0 && lane < J * MT) {
+        const size_t i = lane % MT, j = j0 + lane / MT;
+        if (i < m.m && j < m.n) {
+            float z[1][1] = {{0.f}}, bias[1];
+            for (int p = 0; p < wk; ++p) z[0][0] += part[warp + p][lane];
+            TcRows<float, float, 1, 1> rows;
+            rows.read(m, i, 1, j);
+            load_bias<float>(m, j, bias);
+            rows.write(m, i, 1, j, bias, z);
+        }
+    }
+}
+
+// ---------------------------------------------------------------- out(i,j) = sum_k x(i,k) w(k,j)   (dX)
+//
+// A cluster of 8 blocks takes 32 V neighbouring columns and shares k among its 64 warps; a lane holds V
+// columns' sums for all rows.  The blocks' sums are added in order by the first.
+template <int MT, bool VEC>
+__global__ void __launch_bounds__(kSkThreads) k_skinny_dx(MatmulArgs m) {
+    constexpr int V = VEC ? 4 : 1, AHEAD = 8, COLS = 32 * V;
+    __shared__ __align__(16) float part[kSkWarps][MT][COLS];
+    const uint32_t rank = cluster_rank();
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const size_t j = (size_t)(blockIdx.x / 8) * COLS + (size_t)lane * V;
+    const float* x = static_cast<const float*>(m.a);
+    const float* w = static_cast<const float*>(m.b);
+    float s[MT][V] = {};
+    for (size_t k = rank * kSkWarps + warp; k < m.kk; k += 64 * AHEAD) {
+        float f[AHEAD][V], g[AHEAD][MT];
+        if (VEC && j + V <= m.n && k + 64 * (AHEAD - 1) < m.kk) {
+#pragma unroll
+            for (int u = 0; u < AHEAD; ++u) sk_load<V, VEC>(w + (k + u * 64) * m.bk, j, ~(size_t)0, f[u]);
+        } else {
+#pragma unroll
+            for (int u = 0; u < AHEAD; ++u) sk_load<V, VEC>(w + (k + u * 64) * m.bk, j, k + u * 64 < m.kk ? m.n : 0, f[u]);
+        }
+#pragma unroll
+        for (int u = 0; u < AHEAD; ++u)
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+                g[u][i] = (size_t)i < m.m && k + u * 64 < m.kk ? __ldg(x + i * m.ai + k + u * 64) : 0.f;
+#pragma unroll
+        for (int u = 0; u < AHEAD; ++u)
+            if (k + u * 64 < m.kk)                           // a zero in place of x would hide W's infinities
+#pragma unroll
+                for (int i = 0; i < MT; ++i)
+#pragma unroll
+                    for (int e = 0; e < V; ++e) s[i][e] = fmaf(g[u][i], f[u][e], s[i][e]);
+    }
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int e = 0; e < V; ++e) part[warp][i][lane + e * 32] = s[i][e];
+    __syncthreads();
+    for (int t = threadIdx.x; t < MT * COLS; t += kSkThreads) {
+        float* p = &part[0][0][0] + t;
+        float sum = p[0];
+#pragma unroll
+        for (int q = 1; q < kSkWarps; ++q) sum += p[q * MT * COLS];
+        *p = sum;
+    }
+    cluster_sync();
+    if (rank == 0) {
+        for (int t = threadIdx.x; t < MT * COLS; t += kSkThreads) {
+            const size_t i = t / COLS;
+            const int c = t % COLS;
+            const size_t col = (size_t)(blockIdx.x / 8) * COLS + (size_t)(c % 32) * V + c / 32;
+            if (i >= m.m || col >= m.n) continue;
+            const uint32_t at = smem_u32(&part[0][0][0] + t);
+            float z = 0.f;
+#pragma unroll
+            for (uint32_t r = 0; r < 8; ++r) z += ld_cluster_f(map_rank(at, r));
+            static_cast<float*>(m.out)[i * m.ldo + col] = z;
+        }
+    }
+    __syncwarp();
+    cluster_sync();                                          // the others' sums stay until the first has read them
+}
+
+// ---------------------------------------------------------------- out(i,j) = sum_k z(k,i) x(k,j)   (dW)
+//
+// Few terms: a thread keeps the 16 bytes' columns of x for all terms in registers and goes down 32 rows of
+// the output, which it writes (and, accumulating, reads) once.
+constexpr int kSkRows = 32, kSkRowsAtOnce = 4;
+
+template <class X, class O, int MT, bool VEC>
+__global__ void __launch_bounds__(kSkThreads) k_skinny_dw(MatmulArgs m) {
+    constexpr int V = VEC ? 16 / sizeof(O) : 1, R = kSkRowsAtOnce;
+    const size_t j = ((size_t)blockIdx.x * kSkThreads + threadIdx.x) * V;
+    const size_t i0 = (size_t)blockIdx.y * kSkRows, i1 = min(i0 + kSkRows, m.m);
+    if (j >= m.n) return;
+    const X* z = static_cast<const X*>(m.a);
+    const X* x = static_cast<const X*>(m.b);
+    float f[MT][V];
+#pragma unroll
+    for (int k = 0; k < MT; ++k)
+#pragma unroll
+        for (int e = 0; e < V; ++e) f[k][e] = (size_t)k < m.kk ? to_f(x[k * m.bk + j + e]) : 0.f;
+    for (size_t i = i0; i < i1; i += R) {
+        float s[R][V] = {};
+        if (m.residual) {
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+#pragma unroll
+                for (int e = 0; e < V; ++e)
+                    if (i + r < i1) s[r][e] = load_f<O>(m.residual, (i + r) * m.ldr + j + e);
+        }
+        float g[R][MT];
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int k = 0; k < MT; ++k) g[r][k] = (size_t)k < m.kk && i + r < i1 ? to_f(z[k * m.ak + i + r]) : 0.f;
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            if (i + r >= i1) break;
+            float t[V] = {};
+#pragma unroll
+            for (int k = 0; k < MT; ++k) {
+                if ((size_t)k >= m.kk) break;
+#pragma unroll
+                for (int e = 0; e < V; ++e) t[e] = fmaf(g[r][k], f[k][e], t[e]);
+            }
+            alignas(16) O o[V];
+#pragma unroll
+            for (int e = 0; e < V; ++e) o[e] = from_f<O>(s[r][e] + t[e]);
+            O* p = static_cast<O*>(m.out) + (i + r) * m.ldo + j;
+            if (VEC) {
+                *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(o);
+            } else {
+#pragma unroll
+                for (int e = 0; e < V; ++e) p[e] = o[e];
+            }
+        }
+    }
+}
+
+template <class X, class O, bool VEC>
+static const void* dw_kernel(int mt) {
+    return mt == 1   ? (const void*)k_skinny_dw<X, O, 1, VEC>
+           : mt == 2 ? (const void*)k_skinny_dw<X, O, 2, VEC>
+           : mt == 4 ? (const void*)k_skinny_dw<X, O, 4, VEC>
+                     : (const void*)k_skinny_dw<X, O, 8, VEC>;
+}
+
+bool matmul_is_skinny(size_t rows, sym_dtype_t in, Product p) {
+    if (p == Product::kDw) return rows <= (in == SYM_F32 ? 8u : 4u);
+    return in == SYM_F32 && rows <= (p == Product::kForward ? 4u : 2u);
+}
+
+sym_status_t matmul_skinny(const MatmulArgs& m, sym_dtype_t in, sym_dtype_t out, Product product, int num_sms,
+                           cudaStream_t st) {
+    const size_t few = product == Product::kDw ? m.kk : m.m;
+    const int mt = few <= 1 ? 1 : few <= 2 ? 2 : few <= 4 ? 4 : 8;
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute attr{};
+    cfg.blockDim = dim3(kSkThreads);
+    cfg.stream = st;
+    int wk = 1;
+    MatmulArgs a = m;
+    void* args[] = {&a, &wk};
+    const void* k = nullptr;
+    auto sixteen = [](const void* p, size_t ld) { return (uintptr_t)p % 16 == 0 && ld % 4 == 0; };
+    if (product == Product::kDw) {
+        const size_t v = 16 / dtype_size(out);
+        const bool vec = m.n % v == 0 && (uintptr_t)m.out % 16 == 0 && m.ldo % v == 0;
+        if (in == SYM_F32) k = vec ? dw_kernel<float, float, true>(mt) : dw_kernel<float, float, false>(mt);
+        else if (in == SYM_BF16 && out == SYM_F32)
+            k = vec ? dw_kernel<__nv_bfloat16, float, true>(mt) : dw_kernel<__nv_bfloat16, float, false>(mt);
+        else if (in == SYM_BF16)
+            k = vec ? dw_kernel<__nv_bfloat16, __nv_bfloat16, true>(mt) : dw_kernel<__nv_bfloat16, __nv_bfloat16, false>(mt);
+        else if (out == SYM_F32) k = vec ? dw_kernel<__half, float, true>(mt) : dw_kernel<__half, float, false>(mt);
+        else k = vec ? dw_kernel<__half, __half, true>(mt) : dw_kernel<__half, __half, false>(mt);
+        const size_t gx = ceil_div(m.n, (size_t)kSkThreads * (vec ? v : 1)), gy = ceil_div(m.m, (size_t)kSkRows);
+        // the second grid dimension holds 65535 blocks: more rows go in several launches
+        for (size_t y = 0; y < gy; y += 65535) {
+            const size_t r0 = y * kSkRows;
+            a.m = std::min(m.m - r0, (size_t)65535 * kSkRows);
+            a.a = (const char*)m.a + r0 * dtype_size(in);
+            a.out = (char*)m.out + r0 * m.ldo * dtype_size(out);
+            if (m.residual) a.residual = (const char*)m.residual + r0 * m.ldr * dtype_size(out);
+            cfg.gridDim = dim3((unsigned)gx, (unsigned)std::min(gy - y, (size_t)65535));
+            SYM_CUDA(cudaLaunchKernelExC(&cfg, k, args));
+            count_launch();
+        }
+        return SYM_OK;
+    }
+    if (product == Product::kDx) {
+        const bool vec = sixteen(m.b, m.bk);
+        cfg.gridDim = dim3((unsigned)(8 * ceil_div(m.n, (size_t)32 * (vec ? 4 : 1))));
+        attr.id = cudaLaunchAttributeClusterDimension;
+        attr.val.clusterDim.x = 8;
+        attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+        k = mt == 1 ? (vec ? (const void*)k_skinny_dx<1, true> : (const void*)k_skinny_dx<1, false>)
+                    : (vec ? (const void*)k_skinny_dx<2, true> : (const void*)k_skinny_dx<2, false>);
+    } else {
+        const bool vec = sixteen(m.b, m.bj) && sixteen(m.a, m.m > 1 ? m.ai : 0);
+        // warps that share a column pair's k: as many as it takes to have 32 warps on every SM
+        while (wk < kSkWarps && ceil_div(m.n, (size_t)2) * wk < (size_t)num_sms * 32) wk *= 2;
+        cfg.gridDim = dim3((unsigned)ceil_div(ceil_div(m.n, (size_t)2), (size_t)(kSkWarps / wk)));
+        k = mt == 1   ? (vec ? (const void*)k_skinny_forward<1, true> : (const void*)k_skinny_forward<1, false>)
+            : mt == 2 ? (vec ? (const void*)k_skinny_forward<2, true> : (const void*)k_skinny_forward<2, false>)
+                      : (vec ? (const void*)k_skinny_forward<4, true> : (const void*)k_skinny_forward<4, false>);
+    }
+    SYM_CUDA(cudaLaunchKernelExC(&cfg, k, args));
+    count_launch();
+    return SYM_OK;
+}
+
+}  // namespace symar
