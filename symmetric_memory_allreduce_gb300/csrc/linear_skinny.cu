@@ -4,12 +4,12 @@
 // dX) or writing dW once.  Here each weight is read by one thread, 16 bytes at a time, multiplied with the
 // rows' elements and summed in 32 bits; the partial sums of a long axis are joined in a fixed order.
 //
-// Where this beats the tensor-core kernels (measured, 4096 x 4096 and 16384 x 4096, us; here / there):
-//   32-bit forward  1 row 13.7 / 40, 4 rows 21 / 40, 8 rows 116 / 74 (the larger)    up to 4 rows
-//   32-bit dX       1 row 21 / 39, 2 rows 23 / 39, 4 rows 44 / 39                    up to 2 rows
-//   dW, 32 bits     1 row 72 / 187, 8 rows 147 / 187 (the larger)                    up to 8 rows
-//   dW, 16 bits     1 row 22 / 43 (the larger), 4 rows 13 / 15, 8 rows 36 / 15       up to 4 rows
-//   16-bit forward and dX: 1 row 28 / 24 and 72 / 24 (the larger)                    never
+// Where this beats the tensor-core kernels (measured at 4096 x 4096, us; here / there):
+//   32-bit forward  1 row 13 / 40, 4 rows 21 / 40, 8 rows 35 / 40 (16384 x 4096: 116 / 75)   up to 4 rows
+//   32-bit dX       1 row 13 / 39, 4 rows 16 / 39, 8 rows 20 / 39                             up to 8 rows
+//   32-bit dW       1 row 13 / 52, 8 rows 19 / 52                                             up to 8 rows
+//   16-bit dW       1 row 7 / 15, 4 rows 12 / 15, 8 rows 28 / 15                              up to 4 rows
+//   16-bit forward and dX: 1 row 11 / 11 and 19 / 10                                          never
 #include "linear_tc.cuh"
 
 namespace symar {
@@ -65,7 +65,15 @@ __global__ void __launch_bounds__(kSkThreads) k_skinny_forward(MatmulArgs m, int
                 for (int i = 0; i < MT; ++i) {
                     if ((size_t)i >= m.m) break;
                     float g[V];
-                    sk_load<V, VEC>(x + i * m.ai, k + u * stride, m.kk, g);
+                    const size_t q = k + u * stride;
+                    const float* xi = x + i * m.ai + q;
+                    if (VEC && q + V <= m.kk) {
+                        const float4 t = __ldg(reinterpret_cast<const float4*>(xi));
+                        g[0] = t.x, g[1 % V] = t.y, g[2 % V] = t.z, g[3 % V] = t.w;
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < V; ++e) g[e] = q + e < m.kk ? xi[e] : 0.f;
+                    }
 #pragma unroll
                     for (int e = 0; e < V; ++e) {
                         s[0][i] = fmaf(g[e], f[u][0][e], s[0][i]);
@@ -101,7 +109,7 @@ __global__ void __launch_bounds__(kSkThreads) k_skinny_forward(MatmulArgs m, int
 // columns' sums for all rows.  The blocks' sums are added in order by the first.
 template <int MT, bool VEC>
 __global__ void __launch_bounds__(kSkThreads) k_skinny_dx(MatmulArgs m) {
-    constexpr int V = VEC ? 4 : 1, AHEAD = 8, COLS = 32 * V;
+    constexpr int V = VEC ? 4 : 1, AHEAD = MT == 8 ? 4 : 8, COLS = 32 * V;
     __shared__ __align__(16) float part[kSkWarps][MT][COLS];
     const uint32_t rank = cluster_rank();
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -228,7 +236,7 @@ static const void* dw_kernel(int mt) {
 
 bool matmul_is_skinny(size_t rows, sym_dtype_t in, Product p) {
     if (p == Product::kDw) return rows <= (in == SYM_F32 ? 8u : 4u);
-    return in == SYM_F32 && rows <= (p == Product::kForward ? 4u : 2u);
+    return in == SYM_F32 && rows <= (p == Product::kForward ? 4u : 8u);
 }
 
 sym_status_t matmul_skinny(const MatmulArgs& m, sym_dtype_t in, sym_dtype_t out, Product product, int num_sms,
@@ -276,8 +284,10 @@ sym_status_t matmul_skinny(const MatmulArgs& m, sym_dtype_t in, sym_dtype_t out,
         attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
         cfg.attrs = &attr;
         cfg.numAttrs = 1;
-        k = mt == 1 ? (vec ? (const void*)k_skinny_dx<1, true> : (const void*)k_skinny_dx<1, false>)
-                    : (vec ? (const void*)k_skinny_dx<2, true> : (const void*)k_skinny_dx<2, false>);
+        k = mt == 1   ? (vec ? (const void*)k_skinny_dx<1, true> : (const void*)k_skinny_dx<1, false>)
+            : mt == 2 ? (vec ? (const void*)k_skinny_dx<2, true> : (const void*)k_skinny_dx<2, false>)
+            : mt == 4 ? (vec ? (const void*)k_skinny_dx<4, true> : (const void*)k_skinny_dx<4, false>)
+                      : (vec ? (const void*)k_skinny_dx<8, true> : (const void*)k_skinny_dx<8, false>);
     } else {
         const bool vec = sixteen(m.b, m.bj) && sixteen(m.a, m.m > 1 ? m.ai : 0);
         // warps that share a column pair's k: as many as it takes to have 32 warps on every SM
