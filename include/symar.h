@@ -37,7 +37,8 @@
  *    as SYM_ERR_TIMEOUT from sym_stream_status(); sym_last_error() then names
  *    the wait site: 1 signal wait, 2 counter wait, 3 pull-tile flag, 4 put +
  *    signal / AlltoAll receiver, 5 bulk-copy stage, 6 put + signal batch
- *    order, 7 barrier, 9 linear stage.  No call traps the GPU.
+ *    order, 7 barrier, 9 linear stage, 10 policy loss exchange.  No call traps
+ *    the GPU.
  *  - Windows are owned by the library (sym_window_alloc) or by the caller
  *    (sym_window_register).  Free a window only after every stream that used
  *    it has finished with it; windows must be freed before unloading.

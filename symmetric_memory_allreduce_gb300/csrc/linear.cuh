@@ -108,10 +108,4 @@ sym_status_t matmul_skinny(const MatmulArgs& m, sym_dtype_t in, sym_dtype_t out,
 // How many clusters of 2, 4 and 8 CTAs of these kernels a device holds at once: held[1], held[2], held[4].
 sym_status_t matmul_tc_held(int device, int num_sms, uint32_t* held);
 
-#define SYM_TRY(call)                           \
-    do {                                        \
-        sym_status_t s_ = (call);               \
-        if (s_ != SYM_OK) return s_;            \
-    } while (0)
-
 }  // namespace symar

@@ -11,6 +11,8 @@
 // The sums over a row are held in binary32.  A row of weight 0 is not read:
 // its outputs are 0 whatever stands there.
 #include <cmath>
+#include <map>
+#include <mutex>
 #include <type_traits>
 
 #include "tensor.cuh"
@@ -37,6 +39,7 @@ struct PolicyArgs {
     void* dlogits;             // null: no gradient
     size_t ldd;
     uint32_t* status;
+    uint64_t timeout_ns;
 };
 
 struct RowTerms {
@@ -47,7 +50,7 @@ struct RowTerms {
 // A row's inputs but its logits.
 struct RowInputs {
     float A, old, ref, go;
-    __device__ __forceinline__ RowInputs(const PolicyArgs& a, size_t t) {
+    __device__ __forceinline__ void read(const PolicyArgs& a, size_t t) {
         A = a.adv[t];
         old = a.old_logp[t];
         ref = a.ref_logp ? a.ref_logp[t] : 0.f;
@@ -74,13 +77,16 @@ __device__ __forceinline__ RowTerms row_terms(const PolicyArgs& a, const RowInpu
     return o;
 }
 
+__device__ __forceinline__ float weight_of(const PolicyArgs& a, size_t t) {
+    return t < a.T && a.weights ? a.weights[t] : 1.f;
+}
+__device__ __forceinline__ int64_t target_of(const PolicyArgs& a, size_t t) { return t < a.T ? a.targets[t] : 0; }
+
 // The row's weight, 0 (with the status word set) where its target is no column.
-__device__ __forceinline__ float row_weight(const PolicyArgs& a, size_t t, bool report) {
-    const float w = a.weights ? a.weights[t] : 1.f;
+__device__ __forceinline__ float row_weight(const PolicyArgs& a, size_t t, float w, int64_t y, bool report) {
     if (w == 0.f) return 0.f;
-    const int64_t y = a.targets[t];
     if (y >= 0 && (uint64_t)y < a.V) return w;
-    if (report && threadIdx.x == 0 && (atomicOr(a.status, kStatusBadArg) & kStatusBadArg) == 0) {
+    if (report && (atomicOr(a.status, kStatusBadArg) & kStatusBadArg) == 0) {
         a.status[1] = kSitePolicyTarget;
         a.status[2] = (uint32_t)t;
         a.status[3] = (uint32_t)y;
@@ -88,16 +94,25 @@ __device__ __forceinline__ float row_weight(const PolicyArgs& a, size_t t, bool 
     return 0.f;
 }
 
-// One element of a row, as 16-byte vectors of E elements counted from the 16-byte boundary at or
-// before the row's start: vector v holds elements v*E - phase and on.
+// A row as `head` elements up to the first 16-byte boundary, whole vectors of E elements, and a tail.  The
+// up to 2E-2 elements outside the vectors are the edges, one a thread.
 template <class X>
 struct Row {
     static constexpr int E = 16 / sizeof(X);
     X* p;
-    int phase;
-    __device__ __forceinline__ Row(const void* base, size_t at) {
+    int head, vectors;
+
+    __device__ __forceinline__ Row(const void* base, size_t at, int V) {
         p = const_cast<X*>(static_cast<const X*>(base)) + at;
-        phase = (int)((uintptr_t)p / sizeof(X) % E);
+        head = min((int)((16 - (uintptr_t)p % 16) % 16 / sizeof(X)), V);
+        vectors = (V - head) / E;
+    }
+    __device__ __forceinline__ X* vector(int v) const { return p + head + v * E; }
+    // Index of edge element e, -1 if there are not as many.
+    __device__ __forceinline__ int edge(int e, int V) const {
+        if (e < head) return e;
+        const int j = head + vectors * E + (e - head);
+        return j < V ? j : -1;
     }
 };
 
@@ -161,34 +176,26 @@ __device__ __forceinline__ float max_vector(const uint4& v, float m) {
     return fmaxf(m, fmaxf(x, y));
 }
 
-// Vector v of a row; what lies outside the row's V elements reads as -infinity (weight 0).
 template <class X>
-__device__ __forceinline__ uint4 load_vector(const Row<X>& r, int64_t v, int64_t V) {
-    constexpr int E = Row<X>::E;
-    const int64_t j = v * E - r.phase;
-    if (j >= 0 && j + E <= V) return __ldcs(reinterpret_cast<const uint4*>(r.p + j));
-    const uint32_t inf = minus_inf_bits<X>();
-    uint4 x = make_uint4(inf, inf, inf, inf);
-    X* h = reinterpret_cast<X*>(&x);
-#pragma unroll
-    for (int e = 0; e < E; ++e)
-        if (j + e >= 0 && j + e < V) h[e] = r.p[j + e];
-    return x;
-}
+__device__ __forceinline__ uint4 load_vector(const X* p) { return __ldcs(reinterpret_cast<const uint4*>(p)); }
 
-// Writes the elements of vector v (counted in a row with `phase`) that are inside.
+// To E elements at p, which `aligned` says stand at a 16-byte boundary.
 template <class X>
-__device__ __forceinline__ void store_vector(const Row<X>& r, int phase, int64_t v, int64_t V, const uint4& x) {
-    constexpr int E = Row<X>::E;
-    const int64_t j = v * E - phase;
-    if (phase == r.phase && j >= 0 && j + E <= V) {
-        __stcs(reinterpret_cast<uint4*>(r.p + j), x);
+__device__ __forceinline__ void store_vector(X* p, bool aligned, const uint4& x) {
+    if (aligned) {
+        __stcs(reinterpret_cast<uint4*>(p), x);
         return;
     }
-    const X* h = reinterpret_cast<const X*>(&x);
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-    for (int e = 0; e < E; ++e)
-        if (j + e >= 0 && j + e < V) r.p[j + e] = h[e];
+    for (int k = 0; k < 4; ++k) {
+        if (sizeof(X) == 4) {
+            reinterpret_cast<uint32_t*>(p)[k] = w[k];
+        } else {
+            reinterpret_cast<uint16_t*>(p)[2 * k] = (uint16_t)w[k];
+            reinterpret_cast<uint16_t*>(p)[2 * k + 1] = (uint16_t)(w[k] >> 16);
+        }
+    }
 }
 
 __device__ __forceinline__ float exp2_approx(float x) {      // 2 ulp; below 2^-126: 0
@@ -249,110 +256,330 @@ __device__ __forceinline__ uint4 grad_vector(const uint4& v, F2 c, F2 shift, uin
     return o;
 }
 
-// The target's element, by the thread that wrote its vector, after it.
+// One element's gradient; `target`: whether it is the target's.
 template <class X>
-__device__ __forceinline__ void fix_target(const Row<X>& d, int phase, int64_t v, int64_t y, float c, float xy,
-                                           const RowGrad& g) {
-    const int64_t j = v * Row<X>::E - phase;
-    if (y >= j && y < j + Row<X>::E) d.p[y] = from_f<X>(g.coef - g.coef * exp2_approx(fmaf(xy, c, -g.lse2)));
+__device__ __forceinline__ X grad_one(float x, float c, bool target, const RowGrad& g) {
+    const float v = -g.coef * exp2_approx(fmaf(x, c, -g.lse2));
+    return from_f<X>(target ? g.coef + v : v);
 }
 
-// A cluster of CTAs per row (1, 2, 4 or 8), each with a run of its vectors, VPT a thread at a time,
-// neighbouring threads on neighbouring vectors.  KEEP: the run fits the threads' registers, so the
-// logits are read once and the gradient comes from registers; else they are read again for it.
-template <class X, int THREADS, int VPT, bool KEEP>
-__global__ void __launch_bounds__(THREADS, 1024 / THREADS) k_policy_loss(PolicyArgs a, int64_t run) {
-    __shared__ float s_m[THREADS / 32], s_s[THREADS / 32], s_cm[8], s_cs[8];
-    __shared__ RowGrad s_g;
-    uint32_t rank = 0, C = 1;
+template <class X>
+__device__ __forceinline__ void zero_row(const PolicyArgs& a, size_t t, uint32_t thread, uint32_t threads) {
+    const Row<X> d(a.dlogits, t * a.ldd, (int)a.V);
+    for (int v = (int)thread; v < d.vectors; v += (int)threads) store_vector(d.vector(v), true, make_uint4(0, 0, 0, 0));
+    const int j = thread < 2 * Row<X>::E ? d.edge((int)thread, (int)a.V) : -1;
+    if (j >= 0) d.p[j] = from_f<X>(0.f);
+}
+
+// One thread's: a row's results from its sums, and the gradient's factors.
+template <class X>
+__device__ __forceinline__ RowGrad finish_row(const PolicyArgs& a, uint32_t rank, size_t t, float w, float xy,
+                                              const RowInputs& in, float m, float s) {
+    const float lse = m * a.inv_t + logf(s), logp = xy * a.inv_t - lse;
+    if (rank == 0) {
+        a.logp[t] = logp;
+        a.lse[t] = lse;
+    }
+    return row_grad<X>(in.go * w * row_terms(a, in, logp).slope * a.inv_t, lse);
+}
+
+// One row, as the reading warp hands it to the others.
+struct RowInfo {
+    float w, xy;               // weight (0: the row gets zeros), the target's logit
+    int y;
+    RowInputs in;
+};
+
+constexpr int kLossStages = 3;
+
+template <int VPT>
+constexpr size_t loss_smem(int threads) { return (size_t)kLossStages * threads * VPT * 16 + 16; }
+
+// At most a.timeout_ns, then the device status tells.  The lanes of a warp get one answer.
+__device__ __forceinline__ bool loss_wait(const PolicyArgs& a, uint64_t* bar, uint32_t parity, uint32_t what) {
+    if (__all_sync(~0u, mbar_try_wait(bar, parity))) return true;
+    if (__all_sync(~0u, bounded_wait([&] { return mbar_try_wait(bar, parity); }, a.timeout_ns))) return true;
+    report_timeout(a.status, nullptr, 0, kSitePolicyExchange, what, blockIdx.x);
+    return false;
+}
+
+// A cluster of CTAs (1, 2, 4 or 8) goes over rows `stride` apart, each CTA with a run of their vectors, VPT a
+// thread, neighbouring threads on neighbouring vectors.
+//
+// What bounds a row by itself is not its bytes but the chain from its last exponential to its first
+// gradient: sums over the warps, an exchange in the cluster, logarithm, ratios.  So a CTA works on three
+// rows at once.  One warp reads ahead: it brings runs into a ring of shared-memory stages by bulk copies,
+// with what else a row needs.  The THREADS working threads add up row n from its stage and then write
+// the gradient of row n-1 from its own; nothing but barriers in shared memory ties their warps together.
+// Between the two, one more warp joins row n's sums, exchanges them and forms the gradient's factors.
+template <class X, int THREADS, int VPT>
+__global__ void __launch_bounds__(THREADS + 64, VPT == 8 ? 1 : 1024 / THREADS) k_policy_loss(PolicyArgs a, int run) {
+    constexpr int E = Row<X>::E, W = THREADS / 32;
+    extern __shared__ __align__(16) uint8_t raw[];
+    __shared__ RowInfo s_row[kLossStages];
+    __shared__ float s_edge[kLossStages][2 * E];
+    __shared__ float2 s_part[2][W], s_join[2][8];            // (maximum, sum) of the warps, of the CTAs; [2]: rows by turns
+    __shared__ RowGrad s_g[2];
+    __shared__ __align__(8) uint64_t s_full[kLossStages], s_empty[kLossStages], s_sums[2], s_cluster[2], s_ready[2];
+    uint32_t rank, C;
     asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
     asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(C));
-    const size_t t = blockIdx.x / C;
-    const int64_t V = (int64_t)a.V;
-    const Row<X> x(a.logits, t * a.ld), d(a.dlogits, a.dlogits ? t * a.ldd : 0);
-    const int64_t vectors = (V + x.phase + Row<X>::E - 1) / Row<X>::E;
-    const int64_t v0 = (int64_t)rank * run + threadIdx.x, v1 = min((int64_t)(rank + 1) * run, vectors);
-    uint4 r[VPT];
-    const float w = row_weight(a, t, rank == 0);
-    if (w == 0.f) {                                          // the same in every CTA of the cluster
-        if (rank == 0 && threadIdx.x == 0) a.logp[t] = a.lse[t] = 0.f;
-        if (a.dlogits)
-            for (int64_t v = v0; v < v1; v += THREADS) store_vector<X>(d, x.phase, v, V, make_uint4(0, 0, 0, 0));
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&s_sums[i], W);
+            mbar_init(&s_cluster[i], 1);
+            mbar_init(&s_ready[i], 1);
+        }
+        for (int i = 0; i < kLossStages; ++i) {
+            mbar_init(&s_full[i], 1);
+            mbar_init(&s_empty[i], W + 1);
+        }
+        fence_mbar_init();
+    }
+    __syncthreads();
+    if (C > 1) cluster_sync();                               // remote stores need the others running, barriers set
+    const size_t stride = gridDim.x / C, t0 = blockIdx.x / C;
+    const int V = (int)a.V, warp = (int)threadIdx.x / 32, lane = (int)threadIdx.x % 32;
+    const uint32_t stage_bytes = (uint32_t)(THREADS * VPT) * 16;
+    const float c = a.inv_t * 1.44269504f;
+
+    if (warp == W) {                                         // ---- reads ahead
+        uint32_t st = 0, ph = 1;
+        float w = weight_of(a, t0);
+        int64_t y = target_of(a, t0);
+        for (size_t t = t0; t < a.T; t += stride) {
+            if (!loss_wait(a, &s_empty[st], ph, 1)) return;
+            RowInfo i;
+            i.y = (int)y;
+            i.w = row_weight(a, t, w, y, rank == 0 && lane == 0);
+            uint32_t bytes = 0;
+            if (i.w != 0.f) {
+                const Row<X> x(a.logits, t * a.ld, V);
+                const int n = min((int)(rank + 1) * run, x.vectors) - (int)rank * run;
+                if (n > 0) {
+                    bytes = (uint32_t)n * 16;
+                    if (lane == 0) bulk_load(raw + st * stage_bytes, x.vector((int)rank * run), bytes, &s_full[st]);
+                }
+                // before a gradient in place can replace them
+                i.xy = to_f(x.p[i.y]);
+                const int je = rank == 0 && lane < 2 * E ? x.edge(lane, V) : -1;
+                if (lane < 2 * E) s_edge[st][lane] = je >= 0 ? to_f(x.p[je]) : -INFINITY;
+                i.in.read(a, t);
+            }
+            w = weight_of(a, t + stride);
+            y = target_of(a, t + stride);
+            __syncwarp();
+            if (lane == 0) {
+                s_row[st] = i;
+                mbar_expect_tx(&s_full[st], bytes);
+            }
+            if (++st == kLossStages) st = 0, ph ^= 1;
+        }
         return;
     }
-    const RowInputs in(a, t);
-    const int64_t y = a.targets[t];
-    const float xy = to_f(x.p[y]);                           // before a gradient in place can replace it
-    if (C > 1) cluster_arrive();                             // waited for before the first remote store
-    const float c = a.inv_t * 1.44269504f;
-    float m = -INFINITY, s = 0.f;
-    for (int64_t v = v0; v < v1; v += (int64_t)THREADS * VPT) {
-        const uint32_t inf = minus_inf_bits<X>();
+
+    if (warp == W + 1) {                                     // ---- joins sums, forms the gradient's factors
+        uint32_t st = 0, ph = 0, n = 0;
+        for (size_t t = t0; t < a.T; t += stride) {
+            if (!loss_wait(a, &s_full[st], ph, 2)) return;
+            const RowInfo i = s_row[st];
+            if (i.w != 0.f) {
+                const uint32_t b = n & 1, parity = n >> 1 & 1;
+                if (!loss_wait(a, &s_sums[b], parity, 3)) return;
+                const float2 v = lane < W ? s_part[b][lane] : make_float2(-INFINITY, 0.f);
+                float m = v.x, s = v.y;
+#pragma unroll
+                for (int o = 16; o; o >>= 1) join(c, m, s, __shfl_xor_sync(~0u, m, o), __shfl_xor_sync(~0u, s, o));
+                if (C > 1) {
+                    // to every CTA of the cluster, counted at a barrier there
+                    if (lane == 0) mbar_expect_tx(&s_cluster[b], 8 * C);
+                    if (lane < (int)C)
+                        st_async_f2(map_rank(smem_u32(&s_join[b][rank]), lane), m, s, map_rank(smem_u32(&s_cluster[b]), lane));
+                    if (!loss_wait(a, &s_cluster[b], parity, 4)) return;
+                    const float2 u = lane < (int)C ? s_join[b][lane] : make_float2(-INFINITY, 0.f);
+                    m = u.x, s = u.y;
+#pragma unroll
+                    for (int o = 4; o; o >>= 1) join(c, m, s, __shfl_xor_sync(~0u, m, o), __shfl_xor_sync(~0u, s, o));
+                }
+                if (lane == 0) {
+                    s_g[b] = finish_row<X>(a, rank, t, i.w, i.xy, i.in, m, s);
+                    mbar_arrive(&s_ready[b]);
+                }
+                ++n;
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s_empty[st]);
+            if (++st == kLossStages) st = 0, ph ^= 1;
+        }
+        return;
+    }
+
+    // ---- sums of row n, then gradient of row n - 1
+    const uint32_t inf = minus_inf_bits<X>();
+    const int first = (int)rank * run + (int)threadIdx.x;
+    const bool edges = threadIdx.x < 2 * E;
+    auto vectors = [&](uint32_t st, int end, uint4 (&r)[VPT]) {
+        const uint4* from = reinterpret_cast<const uint4*>(raw + st * stage_bytes) + threadIdx.x;
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) r[k] = first + k * THREADS < end ? from[k * THREADS] : make_uint4(inf, inf, inf, inf);
+    };
+    // the gradient of row t, number n, in stage st; gives the stage back
+    auto gradient = [&](size_t t, uint32_t n, uint32_t st) {
+        const Row<X> x(a.logits, t * a.ld, V);
+        const int end = min((int)(rank + 1) * run, x.vectors);
+        if (!loss_wait(a, &s_ready[n & 1], n >> 1 & 1, 5)) return false;
+        const RowGrad g = s_g[n & 1];
+        if (a.dlogits) {
+            uint4 r[VPT];
+            vectors(st, end, r);
+            const int y = s_row[st].y;
+            const float xy = s_row[st].xy, xe = edges ? s_edge[st][threadIdx.x] : 0.f;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s_empty[st]);
+            X* d = static_cast<X*>(a.dlogits) + t * a.ldd;
+            const bool aligned = (uintptr_t)(d + x.head) % 16 == 0;
+#pragma unroll
+            for (int k = 0; k < VPT; ++k) {
+                const int u = first + k * THREADS;
+                if (u < end) store_vector(d + x.head + u * E, aligned, grad_vector<X>(r[k], f2(c, c), f2(g.shift, g.shift), g.flip));
+            }
+            const int je = rank == 0 && edges ? x.edge((int)threadIdx.x, V) : -1;
+            if (je >= 0) d[je] = grad_one<X>(xe, c, je == y, g);
+            // the target's element, by the thread that has written its vector
+            const int vt = (y - x.head) / E;
+            if (y >= x.head && vt < end && vt >= (int)rank * run && (vt - (int)rank * run) % THREADS == (int)threadIdx.x)
+                d[y] = grad_one<X>(xy, c, true, g);
+        } else {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s_empty[st]);
+        }
+        return true;
+    };
+    uint32_t st = 0, ph = 0, n = 0, st_before = 0;
+    size_t before = a.T;                                     // the row whose gradient is due; a.T: none
+    for (size_t t = t0; t < a.T; t += stride) {
+        if (!loss_wait(a, &s_full[st], ph, 2)) return;
+        if (s_row[st].w == 0.f) {
+            // the gradient that is due holds a stage, which rows without weight must not wait for
+            if (before < a.T && !gradient(before, n - 1, st_before)) return;
+            before = a.T;
+            if (rank == 0 && threadIdx.x == 0) a.logp[t] = a.lse[t] = 0.f;
+            if (a.dlogits) zero_row<X>(a, t, rank * THREADS + threadIdx.x, C * THREADS);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s_empty[st]);
+        } else {
+            const Row<X> x(a.logits, t * a.ld, V);
+            uint4 r[VPT];
+            vectors(st, min((int)(rank + 1) * run, x.vectors), r);
+            const float xe = edges ? s_edge[st][threadIdx.x] : -INFINITY;
+            float m = xe;
+#pragma unroll
+            for (int k = 0; k < VPT; ++k) m = max_vector<X>(r[k], m);
+            m = warp_max(m);
+            const float b = m == -INFINITY ? 0.f : -m * c;   // all -inf: every term is 0
+            F2 sum = f2(exp2_approx(fmaf(xe, c, b)), 0.f);
+#pragma unroll
+            for (int k = 0; k < VPT; ++k) add_vector<X>(r[k], f2(c, c), f2(b, b), sum);
+            float s, s1;
+            split(sum, s, s1);
+            s = warp_sum(s + s1);
+            if (lane == 0) {
+                s_part[n & 1][warp] = make_float2(m, s);
+                mbar_arrive(&s_sums[n & 1]);
+            }
+            if (before < a.T && !gradient(before, n - 1, st_before)) return;
+            before = t;
+            st_before = st;
+            ++n;
+        }
+        if (++st == kLossStages) st = 0, ph ^= 1;
+    }
+    if (before < a.T) gradient(before, n - 1, st_before);
+}
+
+// Rows too wide for a cluster's registers: read once for the sums and again for the gradient.
+constexpr int kWideThreads = 512, kWideVpt = 4;
+
+template <class X>
+__global__ void __launch_bounds__(kWideThreads, 2) k_policy_loss_wide(PolicyArgs a, int run) {
+    constexpr int E = Row<X>::E, THREADS = kWideThreads, VPT = kWideVpt;
+    __shared__ float2 s_part[THREADS / 32], s_join[8];       // (maximum, sum) of the warps, of the CTAs
+    __shared__ RowGrad s_g;
+    uint32_t rank, C;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+    asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(C));
+    cluster_arrive();                                        // waited for before the first remote store
+    const size_t t = blockIdx.x / C;
+    const int V = (int)a.V;
+    const int64_t y = target_of(a, t);
+    const float w = row_weight(a, t, weight_of(a, t), y, rank == 0 && threadIdx.x == 0);
+    if (w == 0.f) {                                          // the same in every CTA of the cluster
+        if (rank == 0 && threadIdx.x == 0) a.logp[t] = a.lse[t] = 0.f;
+        if (a.dlogits) zero_row<X>(a, t, rank * THREADS + threadIdx.x, C * THREADS);
+        __syncwarp();
+        cluster_wait();
+        return;
+    }
+    const uint32_t inf = minus_inf_bits<X>();
+    const Row<X> x(a.logits, t * a.ld, V);
+    const int first = (int)rank * run + (int)threadIdx.x, end = min((int)(rank + 1) * run, x.vectors);
+    const float c = a.inv_t * 1.44269504f, xy = to_f(x.p[y]);
+    const int je = rank == 0 ? x.edge((int)threadIdx.x, V) : -1;
+    const float xe = je >= 0 ? to_f(x.p[je]) : -INFINITY;
+    float m = xe, s = exp2_approx(fmaf(xe, c, xe == -INFINITY ? 0.f : -xe * c));
+    for (int v = first; v < end; v += THREADS * VPT) {
+        uint4 r[VPT];
 #pragma unroll
         for (int k = 0; k < VPT; ++k)
-            r[k] = v + k * THREADS < v1 ? load_vector<X>(x, v + k * THREADS, V) : make_uint4(inf, inf, inf, inf);
+            r[k] = v + k * THREADS < end ? load_vector(x.vector(v + k * THREADS)) : make_uint4(inf, inf, inf, inf);
         float M = m;
 #pragma unroll
         for (int k = 0; k < VPT; ++k) M = max_vector<X>(r[k], M);
-        const float b = M == -INFINITY ? 0.f : -M * c;       // all -inf so far: every term is 0
-        F2 sum = f2(KEEP ? 0.f : s * exp2_approx(fmaf(m, c, b)), 0.f);
+        const float b = M == -INFINITY ? 0.f : -M * c;
+        F2 sum = f2(s * exp2_approx(fmaf(m, c, b)), 0.f);
 #pragma unroll
         for (int k = 0; k < VPT; ++k) add_vector<X>(r[k], f2(c, c), f2(b, b), sum);
         float s1;
         split(sum, s, s1);
         s += s1;
         m = M;
-        if (KEEP) break;
     }
     const float wm = warp_max(m);
     s = warp_sum(s * exp2_approx(fmaf(m, c, wm == -INFINITY ? 0.f : -wm * c)));
-    if (threadIdx.x % 32 == 0) {
-        s_m[threadIdx.x / 32] = wm;
-        s_s[threadIdx.x / 32] = s;
-    }
+    if (threadIdx.x % 32 == 0) s_part[threadIdx.x / 32] = make_float2(wm, s);
     __syncthreads();
-    if (C > 1) cluster_wait();
+    cluster_wait();
     if (threadIdx.x < 32) {
-        constexpr int W = THREADS / 32;
-        m = threadIdx.x < W ? s_m[threadIdx.x] : -INFINITY;
-        s = threadIdx.x < W ? s_s[threadIdx.x] : 0.f;
+        const float2 v = threadIdx.x < THREADS / 32 ? s_part[threadIdx.x] : make_float2(-INFINITY, 0.f);
+        m = v.x, s = v.y;
 #pragma unroll
-        for (int o = 1; o < W; o <<= 1) join(c, m, s, __shfl_xor_sync(~0u, m, o), __shfl_xor_sync(~0u, s, o));
-        if (C > 1 && threadIdx.x < C) {                      // to every CTA of the cluster
-            st_cluster_f32(map_rank(smem_u32(&s_cm[rank]), threadIdx.x), m);
-            st_cluster_f32(map_rank(smem_u32(&s_cs[rank]), threadIdx.x), s);
+        for (int o = 16; o; o >>= 1) join(c, m, s, __shfl_xor_sync(~0u, m, o), __shfl_xor_sync(~0u, s, o));
+        if (threadIdx.x < C) {
+            const uint32_t at = map_rank(smem_u32(&s_join[rank]), threadIdx.x);
+            st_cluster_f32(at, m);
+            st_cluster_f32(at + 4, s);
         }
-    }
-    if (C > 1) {
         __syncwarp();
-        cluster_sync();
     }
+    cluster_sync();
     if (threadIdx.x == 0) {
-        if (C > 1) {
-            m = s_cm[0], s = s_cs[0];
-            for (uint32_t q = 1; q < C; ++q) join(c, m, s, s_cm[q], s_cs[q]);
-        }
-        const float lse = m * a.inv_t + logf(s), logp = xy * a.inv_t - lse;
-        if (rank == 0) {
-            a.logp[t] = logp;
-            a.lse[t] = lse;
-        }
-        if (a.dlogits) s_g = row_grad<X>(in.go * w * row_terms(a, in, logp).slope * a.inv_t, lse);
+        m = s_join[0].x, s = s_join[0].y;
+        for (uint32_t q = 1; q < C; ++q) join(c, m, s, s_join[q].x, s_join[q].y);
+        RowInputs in;
+        in.read(a, t);
+        s_g = finish_row<X>(a, rank, t, w, xy, in, m, s);
     }
-    if (!a.dlogits) return;
     __syncthreads();
+    if (!a.dlogits) return;
     const RowGrad g = s_g;
-    for (int64_t v = v0; v < v1; v += (int64_t)THREADS * VPT) {
-#pragma unroll
-        for (int k = 0; k < VPT; ++k) {
-            const int64_t u = v + k * THREADS;
-            if (u >= v1) break;
-            if (!KEEP) r[k] = load_vector<X>(x, u, V);
-            store_vector<X>(d, x.phase, u, V, grad_vector<X>(r[k], f2(c, c), f2(g.shift, g.shift), g.flip));
-            fix_target<X>(d, x.phase, u, y, c, xy, g);
-        }
-        if (KEEP) break;
-    }
+    X* d = static_cast<X*>(a.dlogits) + t * a.ldd;
+    const bool aligned = (uintptr_t)(d + x.head) % 16 == 0;
+    for (int v = first; v < end; v += THREADS)
+        store_vector(d + x.head + v * E, aligned, grad_vector<X>(load_vector(x.vector(v)), f2(c, c), f2(g.shift, g.shift), g.flip));
+    if (je >= 0) d[je] = grad_one<X>(xe, c, je == (int)y, g);
+    const int vt = ((int)y - x.head) / E;
+    if ((int)y >= x.head && vt < end && vt >= (int)rank * run && (vt - (int)rank * run) % THREADS == (int)threadIdx.x)
+        d[y] = grad_one<X>(xy, c, true, g);
 }
 
 // The gradient alone: a block takes kBackThreads * kBackVectors vectors of a row.
@@ -360,41 +587,46 @@ constexpr int kBackThreads = 256, kBackVectors = 4;
 
 template <class X>
 __global__ void __launch_bounds__(kBackThreads) k_policy_backward(PolicyArgs a, uint32_t blocks_per_row) {
+    constexpr int E = Row<X>::E;
     __shared__ RowGrad s_g;
     const size_t t = blockIdx.x / blocks_per_row;
-    const int64_t V = (int64_t)a.V;
-    const Row<X> x(a.logits, t * a.ld), d(a.dlogits, t * a.ldd);
-    const int64_t v0 = (int64_t)(blockIdx.x % blocks_per_row) * (kBackThreads * kBackVectors) + threadIdx.x;
-    const int64_t vectors = (V + x.phase + Row<X>::E - 1) / Row<X>::E;
-    const float w = row_weight(a, t, blockIdx.x % blocks_per_row == 0);
+    const uint32_t part = blockIdx.x % blocks_per_row;
+    const int V = (int)a.V, v0 = (int)(part * kBackThreads * kBackVectors + threadIdx.x);
+    const Row<X> x(a.logits, t * a.ld, V);
+    const int64_t y = target_of(a, t);
+    const float w = row_weight(a, t, weight_of(a, t), y, part == 0 && threadIdx.x == 0);
     if (w == 0.f) {
-#pragma unroll
-        for (int k = 0; k < kBackVectors; ++k)
-            if (v0 + k * kBackThreads < vectors)
-                store_vector<X>(d, x.phase, v0 + k * kBackThreads, V, make_uint4(0, 0, 0, 0));
+        zero_row<X>(a, t, part * kBackThreads + threadIdx.x, blocks_per_row * kBackThreads);
         return;
     }
     uint4 r[kBackVectors];
 #pragma unroll
     for (int k = 0; k < kBackVectors; ++k)
-        if (v0 + k * kBackThreads < vectors) r[k] = load_vector<X>(x, v0 + k * kBackThreads, V);
-    const int64_t y = a.targets[t];
-    const float c = a.inv_t * 1.44269504f;
+        if (v0 + k * kBackThreads < x.vectors) r[k] = load_vector(x.vector(v0 + k * kBackThreads));
+    const int je = part == 0 ? x.edge((int)threadIdx.x, V) : -1;
+    const float xe = je >= 0 ? to_f(x.p[je]) : 0.f, c = a.inv_t * 1.44269504f;
+    // the target's element, read and written by the thread that has its vector
+    const int vt = ((int)y - x.head) / E;
+    const bool mine = (int)y >= x.head && vt < x.vectors && vt / (kBackThreads * kBackVectors) == (int)part &&
+                      vt % kBackThreads == (int)threadIdx.x;
+    const float xy = mine ? to_f(x.p[y]) : 0.f;
     if (threadIdx.x == 0) {
-        const RowInputs in(a, t);
+        RowInputs in;
+        in.read(a, t);
         s_g = row_grad<X>(in.go * w * row_terms(a, in, a.logp[t]).slope * a.inv_t, a.lse[t]);
     }
     __syncthreads();
     const RowGrad g = s_g;
+    X* d = static_cast<X*>(a.dlogits) + t * a.ldd;
+    const bool aligned = (uintptr_t)(d + x.head) % 16 == 0;
 #pragma unroll
     for (int k = 0; k < kBackVectors; ++k) {
-        const int64_t v = v0 + k * kBackThreads, j = v * Row<X>::E - x.phase;
-        if (v >= vectors) break;
-        const bool target = y >= j && y < j + Row<X>::E;
-        const float xy = target ? to_f(x.p[y]) : 0.f;        // this thread's own vector: not yet replaced
-        store_vector<X>(d, x.phase, v, V, grad_vector<X>(r[k], f2(c, c), f2(g.shift, g.shift), g.flip));
-        if (target) fix_target<X>(d, x.phase, v, y, c, xy, g);
+        const int v = v0 + k * kBackThreads;
+        if (v < x.vectors)
+            store_vector(d + x.head + v * E, aligned, grad_vector<X>(r[k], f2(c, c), f2(g.shift, g.shift), g.flip));
     }
+    if (je >= 0) d[je] = grad_one<X>(xe, c, je == (int)y, g);
+    if (mine) d[y] = grad_one<X>(xy, c, true, g);
 }
 
 // stats = {loss, policy part, kl, weight of clipped rows}, summed in a fixed order by one
@@ -411,7 +643,9 @@ __global__ void __launch_bounds__(THREADS) k_policy_stats(PolicyArgs a) {
         float w = a.weights ? a.weights[t] : 1.f;
         const int64_t y = a.targets[t];
         if (w == 0.f || y < 0 || (uint64_t)y >= a.V) continue;
-        const RowTerms r = row_terms(a, RowInputs(a, t), a.logp[t]);
+        RowInputs in;
+        in.read(a, t);
+        const RowTerms r = row_terms(a, in, a.logp[t]);
         s[0] += w * (r.policy + a.beta * r.kl);
         s[1] += w * r.policy;
         s[2] += w * r.kl;
@@ -428,37 +662,26 @@ __global__ void __launch_bounds__(THREADS) k_policy_stats(PolicyArgs a) {
 struct LossShape {
     int threads, vpt;
     uint32_t cluster;
-    bool keep;
+    bool wide;
 };
 
 static LossShape loss_shape(size_t T, size_t vectors, int num_sms) {
-    LossShape s{128, 2, 1, true};
-    while (s.vpt < 8 && (size_t)s.threads * s.vpt < vectors) s.vpt *= 2;
-    if ((size_t)s.threads * s.vpt < vectors) s = {512, 4, 1, true};
-    if ((size_t)s.threads * s.vpt < vectors) s.vpt = 8;
+    LossShape s{128, 4, 1, false};
+    while (s.threads < 512 && (size_t)s.threads * s.vpt < vectors) s.threads *= 2;
     while (s.cluster < 8 && (size_t)s.threads * s.vpt * s.cluster < vectors) s.cluster *= 2;
-    while (s.cluster < 8 && s.vpt > 2 && T * s.cluster < (size_t)num_sms) s.cluster *= 2, s.vpt /= 2;
-    s.keep = (size_t)s.threads * s.vpt * s.cluster >= vectors;
+    if ((size_t)s.threads * s.vpt * s.cluster < vectors) s.vpt = 8;
+    s.wide = (size_t)s.threads * s.vpt * s.cluster < vectors;
+    while (!s.wide && s.cluster < 8 && s.threads > 128 && T * s.cluster < (size_t)num_sms) s.cluster *= 2, s.threads /= 2;
     return s;
-}
-
-// 16-byte vectors that a row can touch: one more where rows start between their boundaries.
-static size_t row_vectors(const void* logits, size_t ld, size_t rows, size_t vocab, size_t es) {
-    const size_t per = 16 / es;
-    const bool aligned = (uintptr_t)logits % 16 == 0 && (rows == 1 || ld % per == 0);
-    return ceil_div(vocab + (aligned ? 0 : per - 1), per);
 }
 
 template <class X>
 static const void* loss_kernel(const LossShape& s) {
-    if (!s.keep) return (const void*)k_policy_loss<X, 512, 8, false>;
-    if (s.threads == 128)
-        return s.vpt == 2   ? (const void*)k_policy_loss<X, 128, 2, true>
-               : s.vpt == 4 ? (const void*)k_policy_loss<X, 128, 4, true>
-                            : (const void*)k_policy_loss<X, 128, 8, true>;
-    return s.vpt == 2   ? (const void*)k_policy_loss<X, 512, 2, true>
-           : s.vpt == 4 ? (const void*)k_policy_loss<X, 512, 4, true>
-                        : (const void*)k_policy_loss<X, 512, 8, true>;
+    if (s.wide) return (const void*)k_policy_loss_wide<X>;
+    if (s.vpt == 8) return (const void*)k_policy_loss<X, 512, 8>;
+    return s.threads == 128   ? (const void*)k_policy_loss<X, 128, 4>
+           : s.threads == 256 ? (const void*)k_policy_loss<X, 256, 4>
+                              : (const void*)k_policy_loss<X, 512, 4>;
 }
 
 }  // namespace symar
@@ -466,11 +689,12 @@ static const void* loss_kernel(const LossShape& s) {
 using namespace symar;
 
 // A launch with one attribute: a cluster size, or leave to start before the kernel before it has ended.
-static cudaError_t launch_with(const void* kernel, unsigned grid, int threads, void** args, cudaStream_t st,
+static cudaError_t launch_with(const void* kernel, unsigned grid, int threads, size_t smem, void** args, cudaStream_t st,
                                cudaLaunchAttributeID id, uint32_t value) {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute attr{};
     attr.id = id;
@@ -479,6 +703,41 @@ static cudaError_t launch_with(const void* kernel, unsigned grid, int threads, v
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
     return cudaLaunchKernelExC(&cfg, kernel, args);
+}
+
+// How the rows' kernel is launched: threads and shared memory of a CTA, and how many clusters the GPU holds at
+// once (each goes over several rows).
+struct LossLaunch {
+    int threads;
+    size_t smem;
+    uint32_t held;
+};
+
+static sym_status_t loss_launch(int dev, const void* k, const LossShape& sh, LossLaunch* out) {
+    static std::mutex mu;
+    static std::map<std::pair<std::pair<int, uint32_t>, const void*>, LossLaunch> known;
+    std::lock_guard<std::mutex> lk(mu);
+    LossLaunch& l = known[{{dev, sh.cluster}, k}];
+    if (!l.held) {
+        l.threads = sh.wide ? kWideThreads : sh.threads + 64;
+        l.smem = sh.wide ? 0 : sh.vpt == 8 ? loss_smem<8>(sh.threads) : loss_smem<4>(sh.threads);
+        if (l.smem) SYM_CUDA(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)l.smem));
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3(sh.cluster * 64);
+        cfg.blockDim = dim3((unsigned)l.threads);
+        cfg.dynamicSmemBytes = l.smem;
+        cudaLaunchAttribute attr{};
+        attr.id = cudaLaunchAttributeClusterDimension;
+        attr.val.clusterDim.x = sh.cluster;
+        attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+        int c = 0;
+        SYM_CUDA(cudaOccupancyMaxActiveClusters(&c, k, &cfg));
+        l.held = (uint32_t)std::max(c, 1);
+    }
+    *out = l;
+    return SYM_OK;
 }
 
 static sym_status_t check_policy(const PolicyArgs& a, sym_dtype_t dtype, double clip_low, double clip_high,
@@ -518,7 +777,7 @@ sym_status_t sym_policy_loss(const void* logits, size_t ld, size_t rows, size_t 
                              size_t ldd, const float* grad_out, sym_stream_t stream) {
     PolicyArgs a{logits, ld, rows, vocab, targets, old_logp, ref_logp, advantages, weights, grad_out,
                  (float)(1.0 - clip_low), (float)(1.0 + clip_high), (float)kl_coef, (float)(1.0 / temperature),
-                 stats, logp, lse, dlogits, ldd, nullptr};
+                 stats, logp, lse, dlogits, ldd, nullptr, default_timeout_ns()};
     if (!stats) return SYM_ERR_INVALID_ARG;
     sym_status_t s = check_policy(a, dtype, clip_low, clip_high, kl_coef, temperature);
     if (s != SYM_OK) return s;
@@ -529,20 +788,23 @@ sym_status_t sym_policy_loss(const void* logits, size_t ld, size_t rows, size_t 
     cudaStream_t st = (cudaStream_t)stream;
     a.status = ctx->status;
     if (rows) {
-        const size_t vectors = row_vectors(logits, ld, rows, vocab, dtype_size(dtype));
+        const size_t vectors = std::max<size_t>(vocab * dtype_size(dtype) / 16, 1);   // of a row that starts at a boundary
         const LossShape sh = loss_shape(rows, vectors, ctx->num_sms);
-        if (rows * sh.cluster >= (1ull << 31)) return SYM_ERR_UNSUPPORTED;
-        int64_t run = (int64_t)ceil_div(vectors, (size_t)sh.cluster);
+        int run = (int)ceil_div(vectors, (size_t)sh.cluster);
         const void* k = dtype == SYM_F32    ? loss_kernel<float>(sh)
                         : dtype == SYM_BF16 ? loss_kernel<__nv_bfloat16>(sh)
                                             : loss_kernel<__half>(sh);
         void* args[] = {&a, &run};
-        SYM_CUDA(launch_with(k, (unsigned)(rows * sh.cluster), sh.threads, args, st,
+        LossLaunch l;
+        SYM_TRY(loss_launch(dev, k, sh, &l));
+        const size_t clusters = sh.wide ? rows : std::min<size_t>(rows, l.held);
+        if (clusters * sh.cluster >= (1ull << 31)) return SYM_ERR_UNSUPPORTED;
+        SYM_CUDA(launch_with(k, (unsigned)(clusters * sh.cluster), l.threads, l.smem, args, st,
                              cudaLaunchAttributeClusterDimension, sh.cluster));
     }
     {
         void* args[] = {&a};
-        SYM_CUDA(launch_with((const void*)k_policy_stats<kStatsThreads>, 1, kStatsThreads, args, st,
+        SYM_CUDA(launch_with((const void*)k_policy_stats<kStatsThreads>, 1, kStatsThreads, 0, args, st,
                              cudaLaunchAttributeProgrammaticStreamSerialization, 1));
     }
     count_launch(rows ? 2 : 1);
@@ -558,7 +820,7 @@ sym_status_t sym_policy_loss_backward(const void* logits, size_t ld, size_t rows
                                       sym_stream_t stream) {
     PolicyArgs a{logits, ld, rows, vocab, targets, old_logp, ref_logp, advantages, weights, grad_out,
                  (float)(1.0 - clip_low), (float)(1.0 + clip_high), (float)kl_coef, (float)(1.0 / temperature),
-                 nullptr, const_cast<float*>(logp), const_cast<float*>(lse), dlogits, ldd, nullptr};
+                 nullptr, const_cast<float*>(logp), const_cast<float*>(lse), dlogits, ldd, nullptr, default_timeout_ns()};
     sym_status_t s = check_policy(a, dtype, clip_low, clip_high, kl_coef, temperature);
     if (s != SYM_OK) return s;
     if (rows == 0) return SYM_OK;
@@ -569,8 +831,7 @@ sym_status_t sym_policy_loss_backward(const void* logits, size_t ld, size_t rows
     if (!ctx) return SYM_ERR_CUDA;
     a.status = ctx->status;
     cudaStream_t st = (cudaStream_t)stream;
-    const size_t bpr = ceil_div(row_vectors(logits, ld, rows, vocab, dtype_size(dtype)),
-                                (size_t)(kBackThreads * kBackVectors));
+    const size_t bpr = ceil_div(std::max<size_t>(vocab * dtype_size(dtype) / 16, 1), (size_t)(kBackThreads * kBackVectors));
     if (rows * bpr >= (1ull << 31)) return SYM_ERR_UNSUPPORTED;
     const unsigned grid = (unsigned)(rows * bpr);
     switch (dtype) {

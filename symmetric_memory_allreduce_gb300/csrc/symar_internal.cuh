@@ -35,6 +35,7 @@ enum WaitSite : uint32_t {
     kSiteBarrier = 7,          // a rank waited at a barrier for the other ranks' signals
     kSitePolicyTarget = 8,     // policy loss: a row's target is no column of the logits (no wait)
     kSiteLinearStage = 9,      // linear: an operand tile or an accumulator was not ready in time
+    kSitePolicyExchange = 10,  // policy loss: a CTA waited for its cluster's sums of a row
 };
 
 // Per-device context: the status block and the arrival ring used by

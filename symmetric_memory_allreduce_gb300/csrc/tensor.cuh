@@ -53,6 +53,13 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
     return v;
 }
 
+// Two words into a CTA's shared memory of the cluster, their 8 bytes counted at its barrier `bar`.
+__device__ __forceinline__ void st_async_f2(uint32_t addr, float x, float y, uint32_t bar) {
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];" ::"r"(addr), "f"(x),
+                 "f"(y), "r"(bar)
+                 : "memory");
+}
+
 __device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
     asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
@@ -150,6 +157,17 @@ __device__ __forceinline__ void tmem_load(uint32_t addr, float (&v)[16]) {
           "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
         : "r"(addr));
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+
+// Polls pred() without sleeping (a barrier's test waits by itself) until it holds or timeout_ns have passed.
+template <class Pred>
+__device__ __forceinline__ bool bounded_wait(Pred pred, uint64_t timeout_ns) {
+    const uint64_t t0 = globaltimer_ns();
+    for (uint32_t it = 1; it < (1u << 30); ++it) {
+        if (pred()) return true;
+        if ((it & 63u) == 0u && globaltimer_ns() - t0 > timeout_ns) break;
+    }
+    return false;
 }
 
 }  // namespace symar

@@ -7,6 +7,12 @@
 
 #include "symar_internal.cuh"
 
+#define SYM_TRY(call)                           \
+    do {                                        \
+        sym_status_t s_ = (call);               \
+        if (s_ != SYM_OK) return s_;            \
+    } while (0)
+
 namespace symar {
 
 template <class T>

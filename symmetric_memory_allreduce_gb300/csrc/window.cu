@@ -549,7 +549,7 @@ sym_status_t sym_stream_status(sym_stream_t stream) {
     static const char* const kSiteNames[] = {"none", "signal wait", "counter wait", "pull tile flag",
                                              "put+signal/AlltoAll receiver", "bulk-copy stage",
                                              "put+signal batch order", "barrier",
-                                             "policy loss target", "linear stage"};
+                                             "policy loss target", "linear stage", "policy loss exchange"};
     const char* name = st[1] < sizeof kSiteNames / sizeof kSiteNames[0] ? kSiteNames[st[1]] : "?";
     snprintf(g_last_error, sizeof g_last_error, "device status 0x%x at site %u (%s) (%u, %u)", st[0],
              st[1], name, st[2], st[3]);

@@ -10,7 +10,7 @@ import torch
 from _training_util import DTYPES, F64, TINY, UNIT, close, policy64
 
 pytestmark = pytest.mark.gpu
-SHAPES = [(1, 1), (1, 2), (3, 31), (2, 1000), (5, 4097), (7, 8193), (33, 2056), (2, 50003), (1, 131072), (300, 96)]
+SHAPES = [(1, 1), (1, 2), (3, 31), (2, 1000), (5, 4097), (7, 8193), (33, 2056), (2, 50003), (1, 131072), (2, 300_001), (300, 96)]
 HYPER = dict(clip_low=0.2, clip_high=0.3, kl_coef=0.1, temperature=0.8)
 
 
@@ -86,6 +86,20 @@ def test_loss_and_gradient(symar, shape, dtype):
         x = inp["logits"].clone()
         symar.sym_policy_loss(**{**inp, "logits": x}, **out2, dlogits=x, **HYPER)
         assert torch.equal(x, d)
+
+
+@pytest.mark.parametrize("dtype,T,V", [("bf16", 2500, 2056), ("f16", 2500, 96), ("f32", 400, 9001), ("bf16", 90, 70001)])
+def test_many_rows_with_runs_of_masked_ones(symar, dtype, T, V):
+    """More rows than the GPU takes at once, masked in runs of every length."""
+    inp = _inputs(T, V, dtype, T + V)
+    live = torch.rand(T, generator=torch.Generator().manual_seed(T)) < 0.4
+    live[T // 3:T // 2], live[-T // 5:] = False, True
+    inp["weights"] = (live.float() / T).cuda()
+    for d in (torch.full_like(inp["logits"], 7.0), None):
+        out = _outputs(T)
+        symar.sym_policy_loss(**inp, **out, dlogits=d, **HYPER)
+        assert symar.sym_stream_status() == symar.SYM_OK, symar.sym_last_error()
+        _compare(inp, HYPER, out, d)
 
 
 @pytest.mark.parametrize("dtype", list(DTYPES))
