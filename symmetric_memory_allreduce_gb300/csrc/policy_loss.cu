@@ -632,24 +632,39 @@ __global__ void __launch_bounds__(kBackThreads) k_policy_backward(PolicyArgs a, 
 // stats = {loss, policy part, kl, weight of clipped rows}, summed in a fixed order by one
 // block of a launch of its own: a counter that finds the last block of the first launch would
 // have to live somewhere, and two calls in flight (or a replayed graph) would share it.
-constexpr int kStatsThreads = 512;
+constexpr int kStatsThreads = 1024;
 
 template <int THREADS>
 __global__ void __launch_bounds__(THREADS) k_policy_stats(PolicyArgs a) {
     __shared__ float red[THREADS / 32];
     asm volatile("griddepcontrol.wait;" ::: "memory");       // launched while the rows' kernel still runs
     float s[4] = {0.f, 0.f, 0.f, 0.f};
-    for (size_t t = threadIdx.x; t < a.T; t += THREADS) {
-        float w = a.weights ? a.weights[t] : 1.f;
-        const int64_t y = a.targets[t];
-        if (w == 0.f || y < 0 || (uint64_t)y >= a.V) continue;
-        RowInputs in;
-        in.read(a, t);
-        const RowTerms r = row_terms(a, in, a.logp[t]);
-        s[0] += w * (r.policy + a.beta * r.kl);
-        s[1] += w * r.policy;
-        s[2] += w * r.kl;
-        s[3] += r.clipped ? w : 0.f;
+    constexpr int AT_ONCE = 4;                               // rows whose reads leave together
+    for (size_t t0 = threadIdx.x; t0 < a.T; t0 += THREADS * AT_ONCE) {
+        float w[AT_ONCE], logp[AT_ONCE];
+        int64_t y[AT_ONCE];
+        RowInputs in[AT_ONCE];
+#pragma unroll
+        for (int u = 0; u < AT_ONCE; ++u) {
+            const size_t t = t0 + (size_t)u * THREADS;
+            if (t >= a.T) {
+                w[u] = 0.f;
+                continue;
+            }
+            w[u] = weight_of(a, t);
+            y[u] = a.targets[t];
+            logp[u] = a.logp[t];
+            in[u].read(a, t);
+        }
+#pragma unroll
+        for (int u = 0; u < AT_ONCE; ++u) {
+            if (w[u] == 0.f || y[u] < 0 || (uint64_t)y[u] >= a.V) continue;
+            const RowTerms r = row_terms(a, in[u], logp[u]);
+            s[0] += w[u] * (r.policy + a.beta * r.kl);
+            s[1] += w[u] * r.policy;
+            s[2] += w[u] * r.kl;
+            s[3] += r.clipped ? w[u] : 0.f;
+        }
     }
     for (int i = 0; i < 4; ++i) {
         const float v = block_sum<THREADS>(s[i], red);
