@@ -7,8 +7,7 @@
 #include <cmath>
 #include <cstdlib>
 
-#include "linear.cuh"
-#include "tensor.cuh"
+#include "linear_tc.cuh"
 
 namespace symar {
 
@@ -82,6 +81,8 @@ __global__ void __launch_bounds__(kDzThreads, 3) k_linear_dz(DzArgs a) {
     const size_t strip = (a.M + kDzCluster - 1) / kDzCluster;
     const size_t r0 = rank * strip, r1 = min(r0 + strip, a.M);
     cluster_arrive();                                        // waited for before the first remote store
+    launch_next();
+    wait_previous();
     float s[8] = {};
     for (size_t i = r0 + ty; live && i < r1; i += (size_t)ROWS * UNROLL) {
         RowItem<X> dy[UNROLL], z[UNROLL];
@@ -156,6 +157,8 @@ static size_t align_bytes(const void* p, size_t rows, size_t cols, size_t ld, sy
 // 16-bit elements; a warp per row piece of 256, 8 a thread, so stores are 16 bytes and loads coalesced.
 __global__ void __launch_bounds__(256) k_align_rows(const uint16_t* src, size_t ld, size_t rows, size_t cols,
                                                     uint16_t* dst, size_t ldd) {
+    launch_next();
+    wait_previous();
     const size_t row = (size_t)blockIdx.x * 8 + threadIdx.x / 32;
     const size_t c0 = (size_t)blockIdx.y * 256 + (threadIdx.x % 32) * 8;
     if (row >= rows || c0 >= ldd) return;
@@ -176,10 +179,10 @@ static sym_status_t align_operand(const void*& p, size_t& ld, size_t rows, size_
     const size_t ldd = padded(cols);
     const size_t gx = ceil_div(rows, (size_t)8), gy = ceil_div(ldd, (size_t)256);
     if (gy > 65535) return SYM_ERR_UNSUPPORTED;
-    k_align_rows<<<dim3((unsigned)gx, (unsigned)gy), 256, 0, st>>>((const uint16_t*)p, ld, rows, cols, (uint16_t*)ws,
-                                                                   ldd);
+    TcConfig c(1, 256, 0, 1, st);
+    c.cfg.gridDim = dim3((unsigned)gx, (unsigned)gy);
+    SYM_CUDA(cudaLaunchKernelEx(&c.cfg, k_align_rows, (const uint16_t*)p, ld, rows, cols, (uint16_t*)ws, ldd));
     count_launch();
-    SYM_CUDA(cudaGetLastError());
     p = ws;
     ld = ldd;
     ws += bytes;
@@ -397,18 +400,9 @@ sym_status_t sym_linear_backward(const void* dy, size_t lddy, const void* x, siz
                                                                      : dz_kernel<__nv_bfloat16, __nv_bfloat16>(act))
                                             : (grad_dtype == SYM_F32 ? dz_kernel<__half, float>(act)
                                                                      : dz_kernel<__half, __half>(act));
-        cudaLaunchConfig_t cfg{};
-        cfg.gridDim = dim3((unsigned)(ceil_div(N, (size_t)kDzCols) * kDzCluster));
-        cfg.blockDim = dim3(kDzThreads);
-        cfg.stream = st;
-        cudaLaunchAttribute attr{};
-        attr.id = cudaLaunchAttributeClusterDimension;
-        attr.val.clusterDim.x = kDzCluster;
-        attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-        cfg.attrs = &attr;
-        cfg.numAttrs = 1;
+        const TcConfig c((uint32_t)(ceil_div(N, (size_t)kDzCols) * kDzCluster), kDzThreads, 0, kDzCluster, st);
         void* args[] = {&d};
-        SYM_CUDA(cudaLaunchKernelExC(&cfg, k, args));
+        SYM_CUDA(cudaLaunchKernelExC(&c.cfg, k, args));
         count_launch();
     }
     char* at = ws + dz_bytes(M, N, es, act);

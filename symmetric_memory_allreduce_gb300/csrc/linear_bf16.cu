@@ -13,7 +13,7 @@ sym_status_t matmul_tc_bf16(const MatmulArgs& m, sym_dtype_t out, bool a_mn, boo
     return launch_tc_type<__nv_bfloat16>(m, SYM_BF16, out, a_mn, b_mn, {nt, splits}, st);
 }
 
-sym_status_t matmul_tc_held(int device, int num_sms, uint32_t* held) {
+sym_status_t matmul_tc_held(int device, int num_sms, uint32_t* held_out) {
     static std::mutex mu;
     static std::map<int, std::array<uint32_t, 5>> known;
     std::lock_guard<std::mutex> lk(mu);
@@ -24,17 +24,15 @@ sym_status_t matmul_tc_held(int device, int num_sms, uint32_t* held) {
         std::array<uint32_t, 5> n{};
         n[1] = (uint32_t)num_sms / 2;
         for (uint32_t s = 2; s <= 4; s *= 2) {
-            cudaLaunchConfig_t cfg{};
-            cudaLaunchAttribute attr{};
-            tc_config(cfg, attr, 2 * s * 64, s, nullptr);
-            int c = 0;
-            SYM_CUDA(cudaOccupancyMaxActiveClusters(&c, k, &cfg));
-            n[s] = (uint32_t)std::max(c, 0);
+            const TcConfig c(2 * s * 64, kTcThreads, kTcSmem, 2 * s, nullptr);
+            int held = 0;
+            SYM_CUDA(cudaOccupancyMaxActiveClusters(&held, k, &c.cfg));
+            n[s] = (uint32_t)std::max(held, 0);
         }
         it = known.emplace(device, n).first;
         if (trace_on()) fprintf(stderr, "[symar] linear: %u, %u, %u clusters of 2, 4, 8 CTAs at once\n", n[1], n[2], n[4]);
     }
-    std::copy(it->second.begin(), it->second.end(), held);
+    std::copy(it->second.begin(), it->second.end(), held_out);
     return SYM_OK;
 }
 

@@ -185,6 +185,8 @@ __global__ void __launch_bounds__(kF32Threads, 1) k_matmul_f32(const __grid_cons
     cluster_sync();
     tc_fence_after();
     const uint32_t tmem = s->tmem;
+    launch_next();
+    wait_previous();                                                 // the set-up above ran under the kernel ahead
 
     const uint32_t S = a.splits, tiles = a.tiles_i * a.tiles_j;
     const uint32_t first = blockIdx.x / (2 * S), step = gridDim.x / (2 * S);
@@ -399,13 +401,9 @@ sym_status_t matmul_f32(const MatmulArgs& m, bool a_mn, bool b_mn, int nt, uint3
         if (!r) SYM_CUDA(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kF32Smem));
         r = true;
     }
-    cudaLaunchConfig_t cfg{};
-    cudaLaunchAttribute attr{};
-    tc_config(cfg, attr, splits > 1 ? tiles * 2 * splits : 2 * std::min(tiles, pairs), splits, st);
-    cfg.blockDim = dim3(kF32Threads);
-    cfg.dynamicSmemBytes = kF32Smem;
+    const TcConfig c(splits > 1 ? tiles * 2 * splits : 2 * std::min(tiles, pairs), kF32Threads, kF32Smem, 2 * splits, st);
     void* args[] = {&a};
-    SYM_CUDA(cudaLaunchKernelExC(&cfg, k, args));
+    SYM_CUDA(cudaLaunchKernelExC(&c.cfg, k, args));
     count_launch();
     return SYM_OK;
 }

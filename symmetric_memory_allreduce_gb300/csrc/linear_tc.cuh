@@ -301,6 +301,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) k_matmul_tc(const __grid_consta
     cluster_sync();
     tc_fence_after();
     const uint32_t tmem = s->tmem;
+    launch_next();
+    wait_previous();                                                 // the set-up above ran under the kernel ahead
 
     const uint32_t S = a.splits, tiles = a.tiles_i * a.tiles_j;
     const uint32_t first = blockIdx.x / (2 * S), step = gridDim.x / (2 * S);
@@ -485,16 +487,23 @@ inline bool columns_in_eights(const MatmulArgs& m) {
            (!m.pre || ((uintptr_t)m.pre % 16 == 0 && m.ldp % 8 == 0));
 }
 
-inline void tc_config(cudaLaunchConfig_t& cfg, cudaLaunchAttribute& attr, uint32_t grid, uint32_t splits, cudaStream_t st) {
-    cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(kTcThreads);
-    cfg.dynamicSmemBytes = kTcSmem;
-    cfg.stream = st;
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = 2 * splits;
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-}
+// Launch of a kernel whose clusters have 2S CTAs, and which may start under the one ahead (wait_previous).
+struct TcConfig {
+    cudaLaunchConfig_t cfg{};
+    cudaLaunchAttribute attr[2]{};
+    TcConfig(uint32_t grid, int threads, size_t smem, uint32_t cluster, cudaStream_t st) {
+        cfg.gridDim = dim3(grid);
+        cfg.blockDim = dim3((unsigned)threads);
+        cfg.dynamicSmemBytes = smem;
+        cfg.stream = st;
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = cluster;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[1].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 2;
+    }
+};
 
 }  // namespace symar

@@ -68,11 +68,9 @@ sym_status_t launch_tc(const MatmulArgs& m, sym_dtype_t t, uint32_t splits, cuda
         if (dev < 64) ready[vec].fetch_or(1ull << dev, std::memory_order_release);
     }
     const uint32_t pairs = (uint32_t)ctx->num_sms / 2;
-    cudaLaunchConfig_t cfg{};
-    cudaLaunchAttribute attr{};
-    tc_config(cfg, attr, splits > 1 ? tiles * 2 * splits : 2 * std::min(tiles, pairs), splits, st);
+    const TcConfig c(splits > 1 ? tiles * 2 * splits : 2 * std::min(tiles, pairs), kTcThreads, kTcSmem, 2 * splits, st);
     void* args[] = {&a};
-    SYM_CUDA(cudaLaunchKernelExC(&cfg, kernel, args));
+    SYM_CUDA(cudaLaunchKernelExC(&c.cfg, kernel, args));
     count_launch();
     return SYM_OK;
 }

@@ -14,6 +14,12 @@ __device__ __forceinline__ uint32_t cluster_rank() {
     return r;
 }
 
+// A kernel launched with programmatic stream serialisation starts before the one ahead of it in the stream
+// has ended, and must not touch memory until this wait, which lasts until that one has ended and its
+// stores are visible.  launch_next lets the kernel behind start in the same way.
+__device__ __forceinline__ void wait_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void launch_next() { asm volatile("griddepcontrol.launch_dependents;"); }
+
 // True in one lane of a converged warp, the same one every time.
 __device__ __forceinline__ bool elect_lane() {
     uint32_t r;
