@@ -154,40 +154,63 @@ static size_t align_bytes(const void* p, size_t rows, size_t cols, size_t ld, sy
     return ceil_div(rows * padded(cols) * 2, (size_t)256) * 256;
 }
 
+// Up to three operands' copies in one launch.
+struct AlignArgs {
+    struct Item {
+        const uint16_t* src;
+        size_t ld, rows, cols;
+        uint16_t* dst;
+        size_t ldd;
+    } item[3];
+};
+
 // 16-bit elements; a warp per row piece of 256, 8 a thread, so stores are 16 bytes and loads coalesced.
-__global__ void __launch_bounds__(256) k_align_rows(const uint16_t* src, size_t ld, size_t rows, size_t cols,
-                                                    uint16_t* dst, size_t ldd) {
+__global__ void __launch_bounds__(256) k_align_rows(AlignArgs a) {
     launch_next();
     wait_previous();
+    const AlignArgs::Item t = a.item[blockIdx.z];
     const size_t row = (size_t)blockIdx.x * 8 + threadIdx.x / 32;
     const size_t c0 = (size_t)blockIdx.y * 256 + (threadIdx.x % 32) * 8;
-    if (row >= rows || c0 >= ldd) return;
+    if (row >= t.rows || c0 >= t.ldd) return;
     uint16_t v[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = c0 + e < cols ? src[row * ld + c0 + e] : 0;
+    for (int e = 0; e < 8; ++e) v[e] = c0 + e < t.cols ? t.src[row * t.ld + c0 + e] : 0;
     uint4 o;
     o.x = v[0] | (uint32_t)v[1] << 16, o.y = v[2] | (uint32_t)v[3] << 16;
     o.z = v[4] | (uint32_t)v[5] << 16, o.w = v[6] | (uint32_t)v[7] << 16;
-    *reinterpret_cast<uint4*>(dst + row * ldd + c0) = o;
+    *reinterpret_cast<uint4*>(t.dst + row * t.ldd + c0) = o;
 }
 
-// Points `p`, `ld` at an aligned copy of the operand if it is not aligned; `ws` moves past it.
-static sym_status_t align_operand(const void*& p, size_t& ld, size_t rows, size_t cols, sym_dtype_t t, char*& ws,
-                                  cudaStream_t st) {
-    const size_t bytes = align_bytes(p, rows, cols, ld, t);
-    if (!bytes) return SYM_OK;
-    const size_t ldd = padded(cols);
-    const size_t gx = ceil_div(rows, (size_t)8), gy = ceil_div(ldd, (size_t)256);
-    if (gy > 65535) return SYM_ERR_UNSUPPORTED;
-    TcConfig c(1, 256, 0, 1, st);
-    c.cfg.gridDim = dim3((unsigned)gx, (unsigned)gy);
-    SYM_CUDA(cudaLaunchKernelEx(&c.cfg, k_align_rows, (const uint16_t*)p, ld, rows, cols, (uint16_t*)ws, ldd));
-    count_launch();
-    p = ws;
-    ld = ldd;
-    ws += bytes;
-    return SYM_OK;
-}
+// Collects the operands of a call that need an aligned copy and makes the copies.
+struct Aligner {
+    AlignArgs a{};
+    unsigned n = 0;
+    size_t rows = 0, cols = 0;
+    char* ws;
+    explicit Aligner(char* workspace) : ws(workspace) {}
+
+    // Points `p`, `ld` at the copy to be, if the operand is not aligned.
+    void add(const void*& p, size_t& ld, size_t r, size_t c, sym_dtype_t t) {
+        const size_t bytes = align_bytes(p, r, c, ld, t);
+        if (!bytes) return;
+        a.item[n++] = {(const uint16_t*)p, ld, r, c, (uint16_t*)ws, padded(c)};
+        rows = std::max(rows, r);
+        cols = std::max(cols, padded(c));
+        p = ws;
+        ld = padded(c);
+        ws += bytes;
+    }
+    sym_status_t run(cudaStream_t st) const {
+        if (!n) return SYM_OK;
+        const size_t gx = ceil_div(rows, (size_t)8), gy = ceil_div(cols, (size_t)256);
+        if (gy > 65535) return SYM_ERR_UNSUPPORTED;
+        TcConfig c(1, 256, 0, 1, st);
+        c.cfg.gridDim = dim3((unsigned)gx, (unsigned)gy, n);
+        SYM_CUDA(cudaLaunchKernelEx(&c.cfg, k_align_rows, a));
+        count_launch();
+        return SYM_OK;
+    }
+};
 
 // Workspace of the backward call: dZ (rows padded to 16 bytes), then aligned operands.
 static size_t dz_bytes(size_t M, size_t N, size_t es, int act) {
@@ -325,10 +348,10 @@ sym_status_t sym_linear(const void* x, size_t ldx, const void* w, size_t ldw, co
             return SYM_ERR_INVALID_ARG;
         }
     cudaStream_t st = (cudaStream_t)stream;
-    char* ws = (char*)workspace;
-    sym_status_t s = align_operand(x, ldx, M, K, dtype, ws, st);
-    if (s == SYM_OK) s = align_operand(w, ldw, N, K, dtype, ws, st);
-    if (s != SYM_OK) return s;
+    Aligner al((char*)workspace);
+    al.add(x, ldx, M, K, dtype);
+    al.add(w, ldw, N, K, dtype);
+    SYM_TRY(al.run(st));
     MatmulArgs m{x, w, ldx, 1, ldw, 1, M, N, K, bias, residual, ldr, pre, ldp, y, ldy, (int)act};
     return matmul(m, dtype, dtype, Product::kForward, st);
 }
@@ -405,14 +428,13 @@ sym_status_t sym_linear_backward(const void* dy, size_t lddy, const void* x, siz
         SYM_CUDA(cudaLaunchKernelExC(&c.cfg, k, args));
         count_launch();
     }
-    char* at = ws + dz_bytes(M, N, es, act);
-    if ((dx && M && K) || (dw && N && K)) {
-        sym_status_t s = SYM_OK;
+    if (M && N && K && (dx || dw)) {
+        Aligner al(ws + dz_bytes(M, N, es, act));
         const bool skinny = matmul_is_skinny(M, dtype, Product::kDw);
-        if (N && M && dz == dy && (dx || !skinny)) s = align_operand(dz, lddz, M, N, dtype, at, st);
-        if (s == SYM_OK && dw && N && M && !skinny) s = align_operand(x, ldx, M, K, dtype, at, st);
-        if (s == SYM_OK && dx && N && M) s = align_operand(w, ldw, N, K, dtype, at, st);
-        if (s != SYM_OK) return s;
+        if (dz == dy && (dx || !skinny)) al.add(dz, lddz, M, N, dtype);
+        if (dw && !skinny) al.add(x, ldx, M, K, dtype);
+        if (dx) al.add(w, ldw, N, K, dtype);
+        SYM_TRY(al.run(st));
     }
     if (dx && M && K) {
         // dX(m,k) = sum_n dZ(m,n) W(n,k)

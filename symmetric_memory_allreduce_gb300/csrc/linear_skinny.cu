@@ -7,7 +7,7 @@
 // Where this beats the tensor-core kernels (measured at 4096 x 4096, us; here / there):
 //   32-bit forward  1 row 13 / 40, 4 rows 21 / 40, 8 rows 35 / 40 (16384 x 4096: 116 / 75)   up to 4 rows
 //   32-bit dX       1 row 13 / 39, 4 rows 16 / 39, 8 rows 20 / 39                             up to 8 rows
-//   32-bit dW       1 row 13 / 52, 8 rows 19 / 52                                             up to 8 rows
+//   32-bit dW       1 row 13 / 52, 8 rows 19 / 52, 16 rows 23 / 51, 32 rows 35 / 51            up to 48 rows
 //   16-bit dW       1 row 7 / 15, 4 rows 12 / 15, 8 rows 28 / 15                              up to 4 rows
 //   16-bit forward and dX: 1 row 11 / 11 and 19 / 10                                          never
 #include "linear_tc.cuh"
@@ -173,11 +173,11 @@ __global__ void __launch_bounds__(kSkThreads) k_skinny_dx(MatmulArgs m) {
 //
 // Few terms: a thread keeps the 16 bytes' columns of x for all terms in registers and goes down 32 rows of
 // the output, which it writes (and, accumulating, reads) once.
-constexpr int kSkRows = 32, kSkRowsAtOnce = 4;
+constexpr int kSkRows = 32;
 
 template <class X, class O, int MT, bool VEC>
 __global__ void __launch_bounds__(kSkThreads) k_skinny_dw(MatmulArgs m) {
-    constexpr int V = VEC ? 16 / sizeof(O) : 1, R = kSkRowsAtOnce;
+    constexpr int V = VEC ? 16 / sizeof(O) : 1, R = 4;               // rows whose numbers are read at once
     const size_t j = ((size_t)blockIdx.x * kSkThreads + threadIdx.x) * V;
     const size_t i0 = (size_t)blockIdx.y * kSkRows, i1 = min(i0 + kSkRows, m.m);
     if (j >= m.n) return;
@@ -226,16 +226,69 @@ __global__ void __launch_bounds__(kSkThreads) k_skinny_dw(MatmulArgs m) {
     }
 }
 
+// More than 8 terms, 32 bits: a block takes 128 x 128 of the output, a thread 8 x 8 in registers, the terms through
+// shared memory 16 at a time.  Bound by writing dW at 16 terms and by the FMA units from 32 on.
+constexpr int kFewTile = 128, kFewK = 16;
+
+__global__ void __launch_bounds__(kSkThreads) k_few_terms_dw(MatmulArgs m, bool vec) {
+    __shared__ __align__(16) float sz[kFewK][kFewTile], sx[kFewK][kFewTile];
+    const size_t i0 = (size_t)blockIdx.y * kFewTile, j0 = (size_t)blockIdx.x * kFewTile;
+    const float* z = static_cast<const float*>(m.a);
+    const float* x = static_cast<const float*>(m.b);
+    const int tx = threadIdx.x % 16 * 4, ty = threadIdx.x / 16 * 4;      // its quads: tx, tx + 64; rows ty .., ty + 64 ..
+    float s[8][8] = {};
+    for (size_t k0 = 0; k0 < m.kk; k0 += kFewK) {
+        for (int e = threadIdx.x; e < kFewK * kFewTile; e += kSkThreads) {
+            const int k = e / kFewTile, c = e % kFewTile;
+            const bool in = k0 + k < m.kk;
+            sz[k][c] = in && i0 + c < m.m ? z[(k0 + k) * m.ak + i0 + c] : 0.f;
+            sx[k][c] = in && j0 + c < m.n ? x[(k0 + k) * m.bk + j0 + c] : 0.f;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < kFewK; ++k) {
+            const float4 p = *reinterpret_cast<const float4*>(&sz[k][ty]), q = *reinterpret_cast<const float4*>(&sz[k][ty + 64]);
+            const float4 u = *reinterpret_cast<const float4*>(&sx[k][tx]), v = *reinterpret_cast<const float4*>(&sx[k][tx + 64]);
+            const float f[8] = {p.x, p.y, p.z, p.w, q.x, q.y, q.z, q.w}, g[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int r = 0; r < 8; ++r)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) s[r][e] = fmaf(f[r], g[e], s[r][e]);
+        }
+        __syncthreads();
+    }
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+        const size_t i = i0 + ty + (r & 3) + (r >> 2) * 64;
+        if (i >= m.m) continue;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const size_t j = j0 + tx + h * 64;
+            float* p = static_cast<float*>(m.out) + i * m.ldo + j;
+            const float* old = m.residual ? static_cast<const float*>(m.residual) + i * m.ldr + j : nullptr;
+            float t[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) t[e] = s[r][h * 4 + e] + (old && j + e < m.n ? old[e] : 0.f);
+            if (vec && j + 4 <= m.n) {
+                *reinterpret_cast<float4*>(p) = make_float4(t[0], t[1], t[2], t[3]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (j + e < m.n) p[e] = t[e];
+            }
+        }
+    }
+}
+
 template <class X, class O, bool VEC>
 static const void* dw_kernel(int mt) {
     return mt == 1   ? (const void*)k_skinny_dw<X, O, 1, VEC>
            : mt == 2 ? (const void*)k_skinny_dw<X, O, 2, VEC>
-           : mt == 4 ? (const void*)k_skinny_dw<X, O, 4, VEC>
-                     : (const void*)k_skinny_dw<X, O, 8, VEC>;
+                     : (const void*)k_skinny_dw<X, O, 4, VEC>;
 }
 
 bool matmul_is_skinny(size_t rows, sym_dtype_t in, Product p) {
-    if (p == Product::kDw) return rows <= (in == SYM_F32 ? 8u : 4u);
+    if (p == Product::kDw) return rows <= (in == SYM_F32 ? 48u : 4u);
     return in == SYM_F32 && rows <= (p == Product::kForward ? 4u : 8u);
 }
 
@@ -253,9 +306,18 @@ sym_status_t matmul_skinny(const MatmulArgs& m, sym_dtype_t in, sym_dtype_t out,
     const void* k = nullptr;
     auto sixteen = [](const void* p, size_t ld) { return (uintptr_t)p % 16 == 0 && ld % 4 == 0; };
     if (product == Product::kDw) {
+        if (few > 8) {
+            const size_t gx = ceil_div(m.n, (size_t)kFewTile), gy = ceil_div(m.m, (size_t)kFewTile);
+            if (gy > 65535) return SYM_ERR_UNSUPPORTED;
+            k_few_terms_dw<<<dim3((unsigned)gx, (unsigned)gy), kSkThreads, 0, st>>>(m, sixteen(m.out, m.ldo));
+            count_launch();
+            SYM_CUDA(cudaGetLastError());
+            return SYM_OK;
+        }
         const size_t v = 16 / dtype_size(out);
         const bool vec = m.n % v == 0 && (uintptr_t)m.out % 16 == 0 && m.ldo % v == 0;
-        if (in == SYM_F32) k = vec ? dw_kernel<float, float, true>(mt) : dw_kernel<float, float, false>(mt);
+        if (in == SYM_F32 && mt == 8) k = vec ? (const void*)k_skinny_dw<float, float, 8, true> : (const void*)k_skinny_dw<float, float, 8, false>;
+        else if (in == SYM_F32) k = vec ? dw_kernel<float, float, true>(mt) : dw_kernel<float, float, false>(mt);
         else if (in == SYM_BF16 && out == SYM_F32)
             k = vec ? dw_kernel<__nv_bfloat16, float, true>(mt) : dw_kernel<__nv_bfloat16, float, false>(mt);
         else if (in == SYM_BF16)

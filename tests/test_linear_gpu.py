@@ -14,7 +14,7 @@ from _training_util import DTYPES, F64, TINY, UNIT, act64, close, linear64, slop
 pytestmark = pytest.mark.gpu
 ACTS = ["none", "relu", "gelu", "silu"]
 # one row to several tiles; sizes around the tiles' edges (8, 16, 64, 128, 256), odd ones
-SIZES = [(1, 1, 1), (1, 64, 128), (1, 257, 640), (2, 1000, 96), (3, 65, 4100), (4, 2050, 260), (7, 130, 24), (8, 33, 1001), (9, 33, 1001), (16, 512, 2048), (17, 128, 4096),
+SIZES = [(1, 1, 1), (1, 64, 128), (1, 257, 640), (2, 1000, 96), (3, 65, 4100), (4, 2050, 260), (7, 130, 24), (8, 33, 1001), (9, 33, 1001), (13, 300, 1003), (16, 512, 2048), (17, 128, 4096), (32, 131, 260),
          (33, 264, 136), (64, 640, 328), (100, 72, 1000), (127, 129, 65), (128, 256, 64), (129, 257, 63),
          (200, 136, 200), (256, 512, 512), (333, 777, 1001), (1030, 304, 520)]
 
