@@ -70,8 +70,8 @@ __device__ __forceinline__ void store_row(void* p, size_t at, int live, bool vec
 }
 
 template <class X, class O, int ACT>
-__global__ void __launch_bounds__(kDzThreads, 3) k_linear_dz(DzArgs a) {
-    constexpr int LANES = kDzCols / 8, ROWS = kDzThreads / LANES, UNROLL = sizeof(X) == 2 ? 4 : 2;
+__global__ void __launch_bounds__(kDzThreads, 4) k_linear_dz(DzArgs a) {
+    constexpr int LANES = kDzCols / 8, ROWS = kDzThreads / LANES, UNROLL = 2;
     __shared__ float red[ROWS][kDzCols + 4];
     __shared__ float sums[kDzCluster][kDzCols];              // the first block's: every block's sums
     const uint32_t rank = cluster_rank();
@@ -99,10 +99,13 @@ __global__ void __launch_bounds__(kDzThreads, 3) k_linear_dz(DzArgs a) {
             if (r >= r1) continue;
             float d[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                d[e] = dy[u][e];
-                if (ACT != SYM_ACT_NONE) d[e] *= act_slope<X>(z[u][e], ACT);
+            for (int e = 0; e < 8; e += 2) {
+                float a0 = 1.f, a1 = 1.f;
+                if (ACT != SYM_ACT_NONE) act_slope2<X, ACT>(z[u][e], z[u][e + 1], a0, a1);
+                d[e] = dy[u][e] * a0;
+                d[e + 1] = dy[u][e + 1] * a1;
                 s[e] += d[e];
+                s[e + 1] += d[e + 1];
             }
             if (a.dz) store_row<X>(a.dz, r * a.ldz + j, live, a.vec, d);
         }

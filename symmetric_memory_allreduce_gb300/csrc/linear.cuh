@@ -36,53 +36,74 @@ __device__ __forceinline__ float gauss(float z) {
     return e;
 }
 
-// Phi(-|z|) = erfc(|z|/sqrt 2)/2 = e Q(t), e = exp(-z^2/2), t = 1/(1 + 0.3 |z|).  Q is the polynomial of
-// degree 8 without a constant term that is nearest to Phi(-|z|)/e in relative distance for |z| <= 14.5
-// (fitted on 4000 Chebyshev nodes by reweighted least squares: 1.7e-7 off at most); beyond, e is 0.  One
-// exponential and one reciprocal: 3 times as fast as erfcf, and, unlike 1 + erf, exact digits at both ends.
-__device__ __forceinline__ float lower_tail(float z, float e) {
-    const float t = __fdividef(1.f, fmaf(fabsf(z), 0.3f, 1.f));
-    float q = 0.0354238595f;
-    q = fmaf(q, t, -0.156158936f);
-    q = fmaf(q, t, 0.20455757f);
-    q = fmaf(q, t, -0.0520346846f);
-    q = fmaf(q, t, 0.127692095f);
-    q = fmaf(q, t, 0.100175859f);
-    q = fmaf(q, t, 0.120712149f);
-    q = fmaf(q, t, 0.119632006f);
-    return q * t * e;
+// Phi(-|z|) = erfc(|z|/sqrt 2)/2 = e Q(t), e = exp(-z^2/2), t = 1/(1 + 0.3 |z|), for two z.  Q is the
+// polynomial of degree 8 without a constant term that is nearest to Phi(-|z|)/e in relative distance for
+// |z| <= 14.5 (fitted on 4000 Chebyshev nodes by reweighted least squares: 1.7e-7 off at most); beyond, e
+// is 0.  One exponential and one reciprocal: 3 times as fast as erfcf, and, unlike 1 + erf, exact digits at
+// both ends.
+__device__ __forceinline__ void lower_tail2(float z0, float z1, float e0, float e1, float& h0, float& h1) {
+    const F2 t = f2(__fdividef(1.f, fmaf(fabsf(z0), 0.3f, 1.f)), __fdividef(1.f, fmaf(fabsf(z1), 0.3f, 1.f)));
+    auto both = [](float c) { return f2(c, c); };
+    F2 q = fma2(both(0.0354238595f), t, both(-0.156158936f));
+    q = fma2(q, t, both(0.20455757f));
+    q = fma2(q, t, both(-0.0520346846f));
+    q = fma2(q, t, both(0.127692095f));
+    q = fma2(q, t, both(0.100175859f));
+    q = fma2(q, t, both(0.120712149f));
+    q = fma2(q, t, both(0.119632006f));
+    float q0, q1, t0, t1;
+    split(q, q0, q1);
+    split(t, t0, t1);
+    h0 = q0 * t0 * e0;
+    h1 = q1 * t1 * e1;
 }
 
-// X: the type that the value is rounded to; 32-bit ones get the slower, closer forms.
+// Activations of two elements.  X: the type that they are rounded to; 32-bit ones get the slower, closer
+// forms.
+template <class X, int ACT>
+__device__ __forceinline__ void act_value2(float& z0, float& z1) {
+    constexpr bool PRECISE = sizeof(X) == 4;
+    if (ACT == SYM_ACT_RELU) {
+        z0 = z0 < 0.f ? 0.f : z0;
+        z1 = z1 < 0.f ? 0.f : z1;
+    } else if (ACT == SYM_ACT_GELU) {
+        float h0, h1;
+        lower_tail2(z0, z1, gauss<PRECISE>(z0), gauss<PRECISE>(z1), h0, h1);
+        z0 *= z0 < 0.f ? h0 : 1.f - h0;
+        z1 *= z1 < 0.f ? h1 : 1.f - h1;
+    } else if (ACT == SYM_ACT_SILU) {
+        z0 = PRECISE ? z0 / (1.f + expf(-z0)) : __fdividef(z0, 1.f + __expf(-z0));
+        z1 = PRECISE ? z1 / (1.f + expf(-z1)) : __fdividef(z1, 1.f + __expf(-z1));
+    }
+}
+
 template <class X>
 __device__ __forceinline__ float act_value(float z, int act) {
-    constexpr bool PRECISE = sizeof(X) == 4;
-    switch (act) {
-        case SYM_ACT_RELU: return z < 0.f ? 0.f : z;
-        case SYM_ACT_GELU: {
-            const float h = lower_tail(z, gauss<PRECISE>(z));
-            return z * (z < 0.f ? h : 1.f - h);
-        }
-        case SYM_ACT_SILU: return PRECISE ? z / (1.f + expf(-z)) : __fdividef(z, 1.f + __expf(-z));
-    }
+    float other = 0.f;
+    if (act == SYM_ACT_RELU) act_value2<X, SYM_ACT_RELU>(z, other);
+    else if (act == SYM_ACT_GELU) act_value2<X, SYM_ACT_GELU>(z, other);
+    else if (act == SYM_ACT_SILU) act_value2<X, SYM_ACT_SILU>(z, other);
     return z;
 }
 
-template <class X>
-__device__ __forceinline__ float act_slope(float z, int act) {
+template <class X, int ACT>
+__device__ __forceinline__ void act_slope2(float z0, float z1, float& a0, float& a1) {
     constexpr bool PRECISE = sizeof(X) == 4;
-    switch (act) {
-        case SYM_ACT_RELU: return z > 0.f ? 1.f : 0.f;
-        case SYM_ACT_GELU: {
-            const float e = gauss<PRECISE>(z), h = lower_tail(z, e);
-            return fmaf(z * 0.39894228f, e, z < 0.f ? h : 1.f - h);
-        }
-        case SYM_ACT_SILU: {
-            const float p = PRECISE ? 1.f / (1.f + expf(-z)) : __fdividef(1.f, 1.f + __expf(-z));
-            return p * fmaf(z, 1.f - p, 1.f);
-        }
+    if (ACT == SYM_ACT_RELU) {
+        a0 = z0 > 0.f ? 1.f : 0.f;
+        a1 = z1 > 0.f ? 1.f : 0.f;
+    } else if (ACT == SYM_ACT_GELU) {
+        const float e0 = gauss<PRECISE>(z0), e1 = gauss<PRECISE>(z1);
+        float h0, h1;
+        lower_tail2(z0, z1, e0, e1, h0, h1);
+        a0 = fmaf(z0 * 0.39894228f, e0, z0 < 0.f ? h0 : 1.f - h0);
+        a1 = fmaf(z1 * 0.39894228f, e1, z1 < 0.f ? h1 : 1.f - h1);
+    } else if (ACT == SYM_ACT_SILU) {
+        const float p0 = PRECISE ? 1.f / (1.f + expf(-z0)) : __fdividef(1.f, 1.f + __expf(-z0));
+        const float p1 = PRECISE ? 1.f / (1.f + expf(-z1)) : __fdividef(1.f, 1.f + __expf(-z1));
+        a0 = p0 * fmaf(z0, 1.f - p0, 1.f);
+        a1 = p1 * fmaf(z1, 1.f - p1, 1.f);
     }
-    return 1.f;
 }
 
 // linear_bf16.cu, linear_f16.cu: 16-bit operands on the tensor cores, rows of both operands 16-byte

@@ -184,7 +184,10 @@ struct TcRows {
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
-            for (int e = 0; e < W; ++e) z[u][e] = act_value<X>(z[u][e], ACT);
+            for (int e = 0; e < W; e += 2) {
+                if (W > 1) act_value2<X, ACT>(z[u][e], z[u][(e + 1) % W]);
+                else z[u][e] = act_value<X>(z[u][e], ACT);
+            }
     }
 };
 

@@ -291,6 +291,7 @@ struct RowInfo {
 };
 
 constexpr int kLossStages = 3;
+constexpr uint32_t kLossRows = 4;                            // rows on their way between sums and gradient, at most
 
 template <int VPT>
 constexpr size_t loss_smem(int threads) { return (size_t)kLossStages * threads * VPT * 16 + 16; }
@@ -318,14 +319,15 @@ __global__ void __launch_bounds__(THREADS + 64, VPT == 8 ? 1 : 1024 / THREADS) k
     extern __shared__ __align__(16) uint8_t raw[];
     __shared__ RowInfo s_row[kLossStages];
     __shared__ float s_edge[kLossStages][2 * E];
-    __shared__ float2 s_part[2][W], s_join[2][8];            // (maximum, sum) of the warps, of the CTAs; [2]: rows by turns
-    __shared__ RowGrad s_g[2];
-    __shared__ __align__(8) uint64_t s_full[kLossStages], s_empty[kLossStages], s_sums[2], s_cluster[2], s_ready[2];
+    __shared__ float2 s_part[kLossRows][W], s_join[kLossRows][8];    // (maximum, sum) of the warps, of the CTAs
+    __shared__ RowGrad s_g[kLossRows];
+    __shared__ __align__(8) uint64_t s_full[kLossStages], s_empty[kLossStages];
+    __shared__ __align__(8) uint64_t s_sums[kLossRows], s_cluster[kLossRows], s_ready[kLossRows];
     uint32_t rank, C;
     asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
     asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(C));
     if (threadIdx.x == 0) {
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < kLossRows; ++i) {
             mbar_init(&s_sums[i], W);
             mbar_init(&s_cluster[i], 1);
             mbar_init(&s_ready[i], 1);
@@ -384,7 +386,7 @@ __global__ void __launch_bounds__(THREADS + 64, VPT == 8 ? 1 : 1024 / THREADS) k
             if (!loss_wait(a, &s_full[st], ph, 2)) return;
             const RowInfo i = s_row[st];
             if (i.w != 0.f) {
-                const uint32_t b = n & 1, parity = n >> 1 & 1;
+                const uint32_t b = n % kLossRows, parity = n / kLossRows & 1;
                 if (!loss_wait(a, &s_sums[b], parity, 3)) return;
                 const float2 v = lane < W ? s_part[b][lane] : make_float2(-INFINITY, 0.f);
                 float m = v.x, s = v.y;
@@ -427,32 +429,27 @@ __global__ void __launch_bounds__(THREADS + 64, VPT == 8 ? 1 : 1024 / THREADS) k
     auto gradient = [&](size_t t, uint32_t n, uint32_t st) {
         const Row<X> x(a.logits, t * a.ld, V);
         const int end = min((int)(rank + 1) * run, x.vectors);
-        if (!loss_wait(a, &s_ready[n & 1], n >> 1 & 1, 5)) return false;
-        const RowGrad g = s_g[n & 1];
-        if (a.dlogits) {
-            uint4 r[VPT];
-            vectors(st, end, r);
-            const int y = s_row[st].y;
-            const float xy = s_row[st].xy, xe = edges ? s_edge[st][threadIdx.x] : 0.f;
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&s_empty[st]);
-            X* d = static_cast<X*>(a.dlogits) + t * a.ldd;
-            const bool aligned = (uintptr_t)(d + x.head) % 16 == 0;
+        if (!loss_wait(a, &s_ready[n % kLossRows], n / kLossRows & 1, 5)) return false;
+        const RowGrad g = s_g[n % kLossRows];
+        uint4 r[VPT];
+        vectors(st, end, r);
+        const int y = s_row[st].y;
+        const float xy = s_row[st].xy, xe = edges ? s_edge[st][threadIdx.x] : 0.f;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s_empty[st]);
+        X* d = static_cast<X*>(a.dlogits) + t * a.ldd;
+        const bool aligned = (uintptr_t)(d + x.head) % 16 == 0;
 #pragma unroll
-            for (int k = 0; k < VPT; ++k) {
-                const int u = first + k * THREADS;
-                if (u < end) store_vector(d + x.head + u * E, aligned, grad_vector<X>(r[k], f2(c, c), f2(g.shift, g.shift), g.flip));
-            }
-            const int je = rank == 0 && edges ? x.edge((int)threadIdx.x, V) : -1;
-            if (je >= 0) d[je] = grad_one<X>(xe, c, je == y, g);
-            // the target's element, by the thread that has written its vector
-            const int vt = (y - x.head) / E;
-            if (y >= x.head && vt < end && vt >= (int)rank * run && (vt - (int)rank * run) % THREADS == (int)threadIdx.x)
-                d[y] = grad_one<X>(xy, c, true, g);
-        } else {
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&s_empty[st]);
+        for (int k = 0; k < VPT; ++k) {
+            const int u = first + k * THREADS;
+            if (u < end) store_vector(d + x.head + u * E, aligned, grad_vector<X>(r[k], f2(c, c), f2(g.shift, g.shift), g.flip));
         }
+        const int je = rank == 0 && edges ? x.edge((int)threadIdx.x, V) : -1;
+        if (je >= 0) d[je] = grad_one<X>(xe, c, je == y, g);
+        // the target's element, by the thread that has written its vector
+        const int vt = (y - x.head) / E;
+        if (y >= x.head && vt < end && vt >= (int)rank * run && (vt - (int)rank * run) % THREADS == (int)threadIdx.x)
+            d[y] = grad_one<X>(xy, c, true, g);
         return true;
     };
     uint32_t st = 0, ph = 0, n = 0, st_before = 0;
@@ -472,6 +469,10 @@ __global__ void __launch_bounds__(THREADS + 64, VPT == 8 ? 1 : 1024 / THREADS) k
             uint4 r[VPT];
             vectors(st, min((int)(rank + 1) * run, x.vectors), r);
             const float xe = edges ? s_edge[st][threadIdx.x] : -INFINITY;
+            if (!a.dlogits) {                                // nothing comes back to this stage
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&s_empty[st]);
+            }
             float m = xe;
 #pragma unroll
             for (int k = 0; k < VPT; ++k) m = max_vector<X>(r[k], m);
@@ -483,13 +484,17 @@ __global__ void __launch_bounds__(THREADS + 64, VPT == 8 ? 1 : 1024 / THREADS) k
             float s, s1;
             split(sum, s, s1);
             s = warp_sum(s + s1);
+            // without gradients nothing else says that the slot's last row is done with
+            if (!a.dlogits && n >= kLossRows && !loss_wait(a, &s_ready[n % kLossRows], (n / kLossRows & 1) ^ 1, 5)) return;
             if (lane == 0) {
-                s_part[n & 1][warp] = make_float2(m, s);
-                mbar_arrive(&s_sums[n & 1]);
+                s_part[n % kLossRows][warp] = make_float2(m, s);
+                mbar_arrive(&s_sums[n % kLossRows]);
             }
-            if (before < a.T && !gradient(before, n - 1, st_before)) return;
-            before = t;
-            st_before = st;
+            if (a.dlogits) {
+                if (before < a.T && !gradient(before, n - 1, st_before)) return;
+                before = t;
+                st_before = st;
+            }
             ++n;
         }
         if (++st == kLossStages) st = 0, ph ^= 1;
