@@ -216,10 +216,16 @@ __device__ __forceinline__ void add_vector(const uint4& v, F2 c, F2 b, F2& s) {
     }
 }
 
-// Joins two (maximum, sum) pairs.
-__device__ __forceinline__ void join(float c, float& m, float& s, float m2, float s2) {
-    const float M = fmaxf(m, m2), b = M == -INFINITY ? 0.f : M * c;
-    s = s * exp2_approx(fmaf(m, c, -b)) + s2 * exp2_approx(fmaf(m2, c, -b));
+// Joins the (maximum, sum) pairs of LANES neighbouring lanes: all maxima first, so that one exponential a
+// lane is on the way from the pairs to their sum.
+template <int LANES>
+__device__ __forceinline__ void join_lanes(float c, float& m, float& s) {
+    float M = m;
+#pragma unroll
+    for (int o = LANES / 2; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(~0u, M, o));
+    s *= exp2_approx(fmaf(m, c, M == -INFINITY ? 0.f : -M * c));
+#pragma unroll
+    for (int o = LANES / 2; o; o >>= 1) s += __shfl_xor_sync(~0u, s, o);
     m = M;
 }
 
@@ -390,8 +396,7 @@ __global__ void __launch_bounds__(THREADS + 64, VPT == 8 ? 1 : 1024 / THREADS) k
                 if (!loss_wait(a, &s_sums[b], parity, 3)) return;
                 const float2 v = lane < W ? s_part[b][lane] : make_float2(-INFINITY, 0.f);
                 float m = v.x, s = v.y;
-#pragma unroll
-                for (int o = 16; o; o >>= 1) join(c, m, s, __shfl_xor_sync(~0u, m, o), __shfl_xor_sync(~0u, s, o));
+                join_lanes<16>(c, m, s);                     // in lanes 0 to 15, W of which have a pair
                 if (C > 1) {
                     // to every CTA of the cluster, counted at a barrier there
                     if (lane == 0) mbar_expect_tx(&s_cluster[b], 8 * C);
@@ -400,8 +405,7 @@ __global__ void __launch_bounds__(THREADS + 64, VPT == 8 ? 1 : 1024 / THREADS) k
                     if (!loss_wait(a, &s_cluster[b], parity, 4)) return;
                     const float2 u = lane < (int)C ? s_join[b][lane] : make_float2(-INFINITY, 0.f);
                     m = u.x, s = u.y;
-#pragma unroll
-                    for (int o = 4; o; o >>= 1) join(c, m, s, __shfl_xor_sync(~0u, m, o), __shfl_xor_sync(~0u, s, o));
+                    join_lanes<8>(c, m, s);
                 }
                 if (lane == 0) {
                     s_g[b] = finish_row<X>(a, rank, t, i.w, i.xy, i.in, m, s);
@@ -557,8 +561,7 @@ __global__ void __launch_bounds__(kWideThreads, 2) k_policy_loss_wide(PolicyArgs
     if (threadIdx.x < 32) {
         const float2 v = threadIdx.x < THREADS / 32 ? s_part[threadIdx.x] : make_float2(-INFINITY, 0.f);
         m = v.x, s = v.y;
-#pragma unroll
-        for (int o = 16; o; o >>= 1) join(c, m, s, __shfl_xor_sync(~0u, m, o), __shfl_xor_sync(~0u, s, o));
+        join_lanes<32>(c, m, s);
         if (threadIdx.x < C) {
             const uint32_t at = map_rank(smem_u32(&s_join[rank]), threadIdx.x);
             st_cluster_f32(at, m);
@@ -567,12 +570,13 @@ __global__ void __launch_bounds__(kWideThreads, 2) k_policy_loss_wide(PolicyArgs
         __syncwarp();
     }
     cluster_sync();
-    if (threadIdx.x == 0) {
-        m = s_join[0].x, s = s_join[0].y;
-        for (uint32_t q = 1; q < C; ++q) join(c, m, s, s_join[q].x, s_join[q].y);
+    if (threadIdx.x < 32) {
+        const float2 u = threadIdx.x < C ? s_join[threadIdx.x] : make_float2(-INFINITY, 0.f);
+        m = u.x, s = u.y;
+        join_lanes<8>(c, m, s);
         RowInputs in;
         in.read(a, t);
-        s_g = finish_row<X>(a, rank, t, w, xy, in, m, s);
+        if (threadIdx.x == 0) s_g = finish_row<X>(a, rank, t, w, xy, in, m, s);
     }
     __syncthreads();
     if (!a.dlogits) return;
