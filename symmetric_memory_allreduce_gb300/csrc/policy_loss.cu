@@ -33,6 +33,7 @@ struct PolicyArgs {
     const float* weights;      // null: 1
     const float* grad_out;     // device scalar; null: 1
     float lo, hi, beta, inv_t;
+    float c;                   // log2(e) inv_t
     float* stats;
     float* logp;
     float* lse;
@@ -204,7 +205,7 @@ __device__ __forceinline__ float exp2_approx(float x) {      // 2 ulp; below 2^-
     return y;
 }
 
-// Adds exp2(c x - b) of a vector's elements to two sums.
+// Adds exp2(c x + b) of a vector's elements to two sums.
 template <class X>
 __device__ __forceinline__ void add_vector(const uint4& v, F2 c, F2 b, F2& s) {
 #pragma unroll
@@ -216,6 +217,13 @@ __device__ __forceinline__ void add_vector(const uint4& v, F2 c, F2 b, F2& s) {
     }
 }
 
+// b = -c m, rounded, as the shift of a sum's exponents, and the sum mended for that rounding, which all its
+// terms share: m is 0 where there is none (-infinity: every term is 0).
+__device__ __forceinline__ float shift_of(float c, float m) { return m == -INFINITY ? 0.f : -m * c; }
+__device__ __forceinline__ float mend_shift(float c, float m, float b, float s) {
+    return m == -INFINITY ? s : fmaf(s, 0.69314718f * fmaf(-m, c, -b), s);
+}
+
 // Joins the (maximum, sum) pairs of LANES neighbouring lanes: all maxima first, so that one exponential a
 // lane is on the way from the pairs to their sum.
 template <int LANES>
@@ -223,7 +231,7 @@ __device__ __forceinline__ void join_lanes(float c, float& m, float& s) {
     float M = m;
 #pragma unroll
     for (int o = LANES / 2; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(~0u, M, o));
-    s *= exp2_approx(fmaf(m, c, M == -INFINITY ? 0.f : -M * c));
+    s *= exp2_approx(M == -INFINITY ? m : (m - M) * c);
 #pragma unroll
     for (int o = LANES / 2; o; o >>= 1) s += __shfl_xor_sync(~0u, s, o);
     m = M;
@@ -281,7 +289,8 @@ __device__ __forceinline__ void zero_row(const PolicyArgs& a, size_t t, uint32_t
 template <class X>
 __device__ __forceinline__ RowGrad finish_row(const PolicyArgs& a, uint32_t rank, size_t t, float w, float xy,
                                               const RowInputs& in, float m, float s) {
-    const float lse = m * a.inv_t + logf(s), logp = xy * a.inv_t - lse;
+    // logp from the distance to the maximum: one rounding at its own size, not two at lse's
+    const float l = logf(s), lse = fmaf(m, a.inv_t, l), logp = m == -INFINITY ? nanf("") : fmaf(xy - m, a.inv_t, -l);
     if (rank == 0) {
         a.logp[t] = logp;
         a.lse[t] = lse;
@@ -349,7 +358,7 @@ __global__ void __launch_bounds__(THREADS + 64, VPT == 8 ? 1 : 1024 / THREADS) k
     const size_t stride = gridDim.x / C, t0 = blockIdx.x / C;
     const int V = (int)a.V, warp = (int)threadIdx.x / 32, lane = (int)threadIdx.x % 32;
     const uint32_t stage_bytes = (uint32_t)(THREADS * VPT) * 16;
-    const float c = a.inv_t * 1.44269504f;
+    const float c = a.c;
 
     if (warp == W) {                                         // ---- reads ahead
         uint32_t st = 0, ph = 1;
@@ -481,13 +490,13 @@ __global__ void __launch_bounds__(THREADS + 64, VPT == 8 ? 1 : 1024 / THREADS) k
 #pragma unroll
             for (int k = 0; k < VPT; ++k) m = max_vector<X>(r[k], m);
             m = warp_max(m);
-            const float b = m == -INFINITY ? 0.f : -m * c;   // all -inf: every term is 0
+            const float b = shift_of(c, m);
             F2 sum = f2(exp2_approx(fmaf(xe, c, b)), 0.f);
 #pragma unroll
             for (int k = 0; k < VPT; ++k) add_vector<X>(r[k], f2(c, c), f2(b, b), sum);
             float s, s1;
             split(sum, s, s1);
-            s = warp_sum(s + s1);
+            s = mend_shift(c, m, b, warp_sum(s + s1));
             // without gradients nothing else says that the slot's last row is done with
             if (!a.dlogits && n >= kLossRows && !loss_wait(a, &s_ready[n % kLossRows], (n / kLossRows & 1) ^ 1, 5)) return;
             if (lane == 0) {
@@ -532,7 +541,7 @@ __global__ void __launch_bounds__(kWideThreads, 2) k_policy_loss_wide(PolicyArgs
     const uint32_t inf = minus_inf_bits<X>();
     const Row<X> x(a.logits, t * a.ld, V);
     const int first = (int)rank * run + (int)threadIdx.x, end = min((int)(rank + 1) * run, x.vectors);
-    const float c = a.inv_t * 1.44269504f, xy = to_f(x.p[y]);
+    const float c = a.c, xy = to_f(x.p[y]);
     const int je = rank == 0 ? x.edge((int)threadIdx.x, V) : -1;
     const float xe = je >= 0 ? to_f(x.p[je]) : -INFINITY;
     float m = xe, s = exp2_approx(fmaf(xe, c, xe == -INFINITY ? 0.f : -xe * c));
@@ -544,17 +553,17 @@ __global__ void __launch_bounds__(kWideThreads, 2) k_policy_loss_wide(PolicyArgs
         float M = m;
 #pragma unroll
         for (int k = 0; k < VPT; ++k) M = max_vector<X>(r[k], M);
-        const float b = M == -INFINITY ? 0.f : -M * c;
+        const float b = shift_of(c, M);
         F2 sum = f2(s * exp2_approx(fmaf(m, c, b)), 0.f);
 #pragma unroll
         for (int k = 0; k < VPT; ++k) add_vector<X>(r[k], f2(c, c), f2(b, b), sum);
         float s1;
         split(sum, s, s1);
-        s += s1;
+        s = mend_shift(c, M, b, s + s1);
         m = M;
     }
     const float wm = warp_max(m);
-    s = warp_sum(s * exp2_approx(fmaf(m, c, wm == -INFINITY ? 0.f : -wm * c)));
+    s = warp_sum(s * exp2_approx(wm == -INFINITY ? m : (m - wm) * c));
     if (threadIdx.x % 32 == 0) s_part[threadIdx.x / 32] = make_float2(wm, s);
     __syncthreads();
     cluster_wait();
@@ -764,13 +773,14 @@ static sym_status_t loss_launch(int dev, const void* k, const LossShape& sh, Los
     return SYM_OK;
 }
 
-static sym_status_t check_policy(const PolicyArgs& a, sym_dtype_t dtype, double clip_low, double clip_high,
+static sym_status_t check_policy(PolicyArgs& a, sym_dtype_t dtype, double clip_low, double clip_high,
                                  double kl_coef, double temperature) {
     const size_t es = dtype_size(dtype);
     if (!es) return SYM_ERR_INVALID_ARG;
     if (!(temperature > 0) || !std::isfinite(temperature) || !(clip_low >= 0) || !(clip_high >= 0) ||
         !std::isfinite(kl_coef))
         return SYM_ERR_INVALID_ARG;
+    a.c = (float)((double)a.inv_t * 1.4426950408889634);
     if (a.T >= (1ull << 31) || a.V >= (1ull << 31)) return SYM_ERR_UNSUPPORTED;
     if (a.T == 0) return SYM_OK;
     if (a.V == 0 || a.ld < a.V || (a.dlogits && a.ldd < a.V)) return SYM_ERR_INVALID_ARG;
@@ -800,7 +810,7 @@ sym_status_t sym_policy_loss(const void* logits, size_t ld, size_t rows, size_t 
                              double kl_coef, double temperature, float* stats, float* logp, float* lse, void* dlogits,
                              size_t ldd, const float* grad_out, sym_stream_t stream) {
     PolicyArgs a{logits, ld, rows, vocab, targets, old_logp, ref_logp, advantages, weights, grad_out,
-                 (float)(1.0 - clip_low), (float)(1.0 + clip_high), (float)kl_coef, (float)(1.0 / temperature),
+                 (float)(1.0 - clip_low), (float)(1.0 + clip_high), (float)kl_coef, (float)(1.0 / temperature), 0.f,
                  stats, logp, lse, dlogits, ldd, nullptr, default_timeout_ns()};
     if (!stats) return SYM_ERR_INVALID_ARG;
     sym_status_t s = check_policy(a, dtype, clip_low, clip_high, kl_coef, temperature);
@@ -843,7 +853,7 @@ sym_status_t sym_policy_loss_backward(const void* logits, size_t ld, size_t rows
                                       const float* lse, void* dlogits, size_t ldd, const float* grad_out,
                                       sym_stream_t stream) {
     PolicyArgs a{logits, ld, rows, vocab, targets, old_logp, ref_logp, advantages, weights, grad_out,
-                 (float)(1.0 - clip_low), (float)(1.0 + clip_high), (float)kl_coef, (float)(1.0 / temperature),
+                 (float)(1.0 - clip_low), (float)(1.0 + clip_high), (float)kl_coef, (float)(1.0 / temperature), 0.f,
                  nullptr, const_cast<float*>(logp), const_cast<float*>(lse), dlogits, ldd, nullptr, default_timeout_ns()};
     sym_status_t s = check_policy(a, dtype, clip_low, clip_high, kl_coef, temperature);
     if (s != SYM_OK) return s;
