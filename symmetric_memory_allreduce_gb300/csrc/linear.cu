@@ -5,7 +5,6 @@
 //   backward  dZ = dY * act'(Z),  dX = dZ W,  dW = dZ^T X,  db = sum_m dZ
 // X is M x K, W is N x K, Y is M x N, all with rows of contiguous elements.
 #include <cmath>
-#include <cstdlib>
 
 #include "linear_tc.cuh"
 
@@ -255,9 +254,6 @@ static void tc_shape(const MatmulArgs& m, bool f32, bool f32_out, bool b_mn, con
             if (t < best) best = t, *nt_out = nt, *splits_out = s;
         }
     }
-#ifdef TC_SWEEP
-    if (getenv("TC_NT")) *nt_out = atoi(getenv("TC_NT")), *splits_out = atoi(getenv("TC_S"));
-#endif
 }
 
 // A product without terms: the epilogue of zero.
