@@ -402,7 +402,8 @@ sym_status_t sym_counter_reset(sym_win_t w, int rank, uint32_t counter_id, sym_s
  * act: none, relu, gelu = z/2 (1 + erf(z/sqrt 2)), silu = z/(1 + exp(-z)).
  * M = 0 or N = 0 does nothing; K = 0 leaves act(bias) + residual.  y may be
  * `residual` itself (same pointer and stride).  BF16 and F16 run on the
- * tensor cores, F32 on the FMA units.  `workspace` holds operands whose rows
+ * tensor cores; F32 too, as three bf16 parts an element with sums in 32 bits
+ * (a few rows on the FMA units).  `workspace` holds 16-bit operands whose rows
  * are not 16-byte aligned, copied to rows that are; sym_linear_workspace says
  * how many bytes it has to have (0 when every row is aligned).
  * Errors: INVALID_ARG, UNSUPPORTED (a size of 2^31 or more), CUDA. */
